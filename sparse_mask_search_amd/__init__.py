@@ -16,7 +16,10 @@ from __future__ import annotations
 
 from ._lib import (F32, BF16, TsenorError, compress24, exact, lib, library_path, mask,
                    mask_batched, mask_noalloc, memory_pass, round_mask, spmm24, unpack, version)
+from ._fp8 import (DenseFp8, Sparse24Fp8, compress24_fp8, compress24_fp8_both, gemm_fp8,
+                   moe24_fp8, quant_fp8, quant_fp8_both, spmm24_fp8)
 
 __all__ = ["F32", "BF16", "TsenorError", "compress24", "exact", "lib", "library_path", "mask",
            "mask_batched", "mask_noalloc", "memory_pass", "round_mask", "spmm24", "unpack",
-           "version"]
+           "version", "DenseFp8", "Sparse24Fp8", "compress24_fp8", "compress24_fp8_both",
+           "gemm_fp8", "moe24_fp8", "quant_fp8", "quant_fp8_both", "spmm24_fp8"]

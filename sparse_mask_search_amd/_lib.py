@@ -66,6 +66,22 @@ def lib():
         l.tsenor_mask_batched_ex.restype = _I
         l.tsenor_bench_memory_pass.argtypes = [_P, _I, _I64, _I64, _I64, _I, _P, _P]
         l.tsenor_bench_memory_pass.restype = _I
+        l.tsenor_quant_fp8.argtypes = [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P]
+        l.tsenor_quant_fp8.restype = _I
+        l.tsenor_compress24_fp8.argtypes = [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P,
+                                            _P, _P, _P, _P, _P]
+        l.tsenor_compress24_fp8.restype = _I
+        l.tsenor_spmm24_fp8.argtypes = [_P, _I, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I, _I64,
+                                        _P]
+        l.tsenor_spmm24_fp8.restype = _I
+        l.tsenor_gemm_fp8.argtypes = [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _P]
+        l.tsenor_gemm_fp8.restype = _I
+        l.tsenor_moe24_fp8_workspace.argtypes = [_I64, _I64, _I64, _I64, _I]
+        l.tsenor_moe24_fp8_workspace.restype = ctypes.c_size_t
+        l.tsenor_moe24_fp8.argtypes = [_P, _I64, _I64, _I64, _P, _I64, _I64, _I, _P, _P, _P, _P, _P,
+                                       _P, _P, _P, _P, _I64, _P, ctypes.c_size_t, _P, _I64, _P, _P,
+                                       _P]
+        l.tsenor_moe24_fp8.restype = _I
         l.tsenor_status_str.argtypes = [_I]
         l.tsenor_status_str.restype = ctypes.c_char_p
         l.tsenor_last_error.argtypes = []

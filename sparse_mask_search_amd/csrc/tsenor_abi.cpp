@@ -237,6 +237,8 @@ int check_finite(DeviceState& st, hipStream_t s, const void* p, int bf16, int64_
 
 }  // namespace
 
+int tsenor::hip_error(int error, const char* where) { return hip_fail((hipError_t)error, where); }
+
 extern "C" {
 
 int tsenor_mask(const void* W, int dtype, int64_t rows, int64_t cols, int64_t ld, int N, int M,
@@ -588,7 +590,7 @@ const char* tsenor_status_str(int status) {
     switch (status) {
         case TSENOR_OK: return "ok";
         case TSENOR_ERR_NULL: return "required pointer is NULL";
-        case TSENOR_ERR_SHAPE: return "bad shape (rows/cols must be positive multiples of M, ld >= cols)";
+        case TSENOR_ERR_SHAPE: return "bad shape, leading dimension or alignment (masks: rows/cols positive multiples of M, ld >= cols)";
         case TSENOR_ERR_NM: return "bad N:M (M in {4,8,16,32}, 1 <= N <= M)";
         case TSENOR_ERR_PARAM: return "bad parameter (tau finite >= 0, iters >= 1, ls_steps >= 0)";
         case TSENOR_ERR_DTYPE: return "bad dtype (TSENOR_F32 or TSENOR_BF16)";

@@ -1,0 +1,115 @@
+// tsenor_fp8_device.h -- device helpers shared by the 8-bit kernels: block
+// scales, conversion to e4m3, element loads.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace tsenor {
+namespace fp8 {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kBlock = 128;  // entries that share a scale along a row
+
+__host__ __device__ __forceinline__ int64_t pad128(int64_t k) { return (k + 127) / 128 * 128; }
+
+__device__ __forceinline__ uint32_t float_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
+
+__device__ __forceinline__ float widen(uint16_t b) { return bits_float((uint32_t)b << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+
+// |x| as an integer that orders like the magnitude; 0 for infinities and NaN.
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+    const uint32_t a = float_bits(x) & 0x7FFFFFFFu;
+    return a < 0x7F800000u ? a : 0u;
+}
+
+// The scale exponent s of a block: least s >= -127 with amax <= 448 * 2^s.
+// With amax = 1.f * 2^(E-127) and 448 = 1.75 * 2^8, s = E-135 if 1.f <= 1.75
+// and E-134 otherwise; subnormal amax (E = 0) clamps.
+__device__ __forceinline__ int scale_exponent(uint32_t amax) {
+    const int E = (int)(amax >> 23);
+    const int s = E - ((amax & 0x7FFFFFu) <= 0x600000u ? 135 : 134);
+    return amax == 0u ? 0 : (s < -127 ? -127 : s);
+}
+
+// 2^-s for the exponents scale_exponent gives (-127 .. 120): always normal.
+__device__ __forceinline__ float inverse_scale(int s) { return bits_float((uint32_t)(127 - s) << 23); }
+
+// 2^e for two scale bytes a and b (e = a + b - 254), clamped to [0, 2^127]:
+// the factor of a block's sum.  Subnormal powers down to 2^-149 are exact.
+__device__ __forceinline__ float scale_product(int a, int b) {
+    const int e = a + b - 127;  // exponent field of the product
+    if (e >= 1) return bits_float((uint32_t)(e > 254 ? 254 : e) << 23);
+    return e > -23 ? bits_float(0x400000u >> -e) : 0.f;
+}
+
+// x * 2^-s before the conversion; infinities become NaN like NaN itself.
+__device__ __forceinline__ float scaled(float x, float inv) {
+    return (float_bits(x) & 0x7F800000u) == 0x7F800000u ? bits_float(0x7FC00000u) : x * inv;
+}
+
+// Four e4m3 numbers, nearest even.  |arguments| <= 448 or NaN.
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
+// fp32 to bf16, nearest even (one instruction on gfx950).
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return (uint32_t)to_bf16(lo) | ((uint32_t)to_bf16(hi) << 16);
+}
+
+// Entries c .. c+7 of a row of `cols` entries (zeros behind it).  vec: the row
+// may be read 16 bytes at a time.
+__device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t cols, bool vec,
+                                      uint16_t v[8]) {
+    if (vec && c + 8 <= cols) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(row + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = (uint16_t)w[i];
+            v[2 * i + 1] = (uint16_t)(w[i] >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : (uint16_t)0;
+    }
+}
+__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, bool vec,
+                                      float v[8]) {
+    if (vec && c + 8 <= cols) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(row + c);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(row + c + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.f;
+    }
+}
+
+// Maximum over the 16 lanes of a row of lanes.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+        const uint32_t o = __shfl_xor(v, d, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+}  // namespace fp8
+}  // namespace tsenor

@@ -73,4 +73,46 @@ int launch_compress24(const uint16_t* W, int64_t ld, const uint32_t* mask, int64
 int launch_spmm24(const uint16_t* X, int64_t ldx, const uint16_t* vals, const uint32_t* meta,
                   float* Y, int64_t ldy, int64_t n, int64_t m, int64_t k, void* stream);
 
+// Builders of the 8-bit operands (tsenor_fp8_operands.hip).
+int launch_quant_fp8(const void* X, int bf16, int64_t rows, int64_t cols, int64_t ldx,
+                     uint8_t* values, uint8_t* scales, uint8_t* values_t, uint8_t* scales_t,
+                     void* stream);
+int launch_compress24_fp8(const void* W, int bf16, int64_t batch, int64_t stride, int64_t rows,
+                          int64_t cols, int64_t ld, const uint32_t* mask, uint8_t* values,
+                          uint32_t* meta, uint8_t* scales, uint8_t* values_t, uint32_t* meta_t,
+                          uint8_t* scales_t, int* bad, int* bad_t, void* stream);
+
+// Products of 8-bit operands (tsenor_fp8_gemm.hip).
+int launch_spmm24_fp8(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx,
+                      const uint8_t* values, const uint32_t* meta, const uint8_t* scales, int64_t m,
+                      int64_t k, void* Y, int bf16y, int64_t ldy, void* stream);
+int launch_gemm_fp8(const uint8_t* A, const uint8_t* as, int64_t p, const uint8_t* B,
+                    const uint8_t* bs, int64_t q, int64_t k, const uint32_t* mask, void* C,
+                    int bf16c, int64_t ldc, void* stream);
+
+// A mixture-of-experts layer (tsenor_fp8_moe.hip).
+struct Operand24 {
+    const uint8_t* values;
+    const uint32_t* meta;
+    const uint8_t* scales;
+};
+struct MoeJob {
+    const uint16_t* x;
+    const uint16_t* router;
+    Operand24 gate, up, down;
+    int64_t n, d, f, experts, ldx, ldr, ldy;
+    int topk;
+    double* logits;    // workspace: [n][experts]
+    uint16_t* xpad;    // workspace: [n][d padded to 128]
+    uint16_t* hidden;  // workspace: [n topk][f padded to 128]
+    int* ids;          // workspace: [n topk]
+    uint16_t* y;
+    int* ids_out;      // or nullptr
+    float* weights_out;
+};
+int launch_moe24_fp8(const MoeJob& job, void* stream);
+
+// Records the message of a HIP error (tsenor_last_error) and gives TSENOR_ERR_HIP.
+int hip_error(int error, const char* where);
+
 }  // namespace tsenor
