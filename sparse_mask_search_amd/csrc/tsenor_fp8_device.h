@@ -46,8 +46,9 @@ __device__ __forceinline__ float inverse_scale(int s) { return bits_float((uint3
 // the factor of a block's sum.  Subnormal powers down to 2^-149 are exact.
 __device__ __forceinline__ float scale_product(int a, int b) {
     const int e = a + b - 127;  // exponent field of the product
-    if (e >= 1) return bits_float((uint32_t)(e > 254 ? 254 : e) << 23);
-    return e > -23 ? bits_float(0x400000u >> -e) : 0.f;
+    const uint32_t normal = (uint32_t)min(e, 254) << 23;
+    const uint32_t subnormal = 0x400000u >> min(max(-e, 0), 31);
+    return bits_float(e >= 1 ? normal : subnormal);
 }
 
 // x * 2^-s before the conversion; infinities become NaN like NaN itself.
@@ -99,6 +100,57 @@ __device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols,
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.f;
     }
+}
+
+// Direct loads from global memory to LDS, from a uniform base plus the lane's
+// offset: lane l's 16 bytes (or 4, or its byte widened to 32 bits) land at the LDS
+// base + 16 l (4 l).  Written in asm because the
+// compiler cannot tell the buffers of a ring apart and would wait for every
+// outstanding direct load before each LDS read; the kernels wait for them
+// themselves (vmcnt) before the barrier that publishes a buffer.  No register
+// receives data.  M0 carries the LDS base; the clobber tells the compiler.
+typedef __attribute__((address_space(3))) void lds_void_t;
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(const lds_void_t*)p;
+}
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // M0 is a reserved register; see above
+__device__ __forceinline__ void dma16(const void* base, uint32_t offset, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2"
+                 :: "v"(offset), "s"(lds_base), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t offset, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, %2"
+                 :: "v"(offset), "s"(lds_base), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_byte(const void* base, uint32_t offset, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, %2"
+                 :: "v"(offset), "s"(lds_base), "s"(base) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Tile (tm, tn) of workgroup `bid` in a tiles_m x tiles_n grid.  Workgroups go
+// to the chip's 8 XCDs round robin and each XCD has its own L2, so XCD x gets a
+// contiguous range of an order that walks groups of up to 8 m-tiles column by
+// column: the tiles that it runs at one time form a compact block of the grid
+// and share their operands' rows.  A bijection for any grid.
+__device__ __forceinline__ void tile_of(int64_t bid, int64_t tiles_m, int64_t tiles_n, int64_t& tm,
+                                        int64_t& tn) {
+    constexpr int64_t kXcd = 8, kGroup = 8;
+    const int64_t nb = tiles_m * tiles_n, x = bid % kXcd, rest = nb % kXcd;
+    const int64_t t = x * (nb / kXcd) + (x < rest ? x : rest) + bid / kXcd;
+    const int64_t grp = t / (kGroup * tiles_n), first = grp * kGroup;
+    const int64_t gm = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+    const int64_t r = t - grp * kGroup * tiles_n;
+    tm = first + r % gm;
+    tn = r / gm;
+}
+
+// The same value, unknown to the compiler: what is computed from it inside a loop
+// stays there, where it costs an instruction, and not in a register across the loop.
+__device__ __forceinline__ int opaque(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // Maximum over the 16 lanes of a row of lanes.
