@@ -45,87 +45,150 @@ __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
     return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
-// Eight bf16 entries as e4m3 after scaling.
-__device__ __forceinline__ u32x2 quant8(const uint16_t v[8], float inv) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = scaled(widen(v[i]), inv);
-    return u32x2{pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7])};
+// Two bf16 entries (a 32-bit word) times inv, as fp32.
+__device__ __forceinline__ void scale2(uint32_t w, float inv, float* lo, float* hi) {
+    *lo = bits_float(w << 16) * inv;
+    *hi = bits_float(w & 0xFFFF0000u) * inv;
 }
 
 // This lane's part of one block of a bf16 row (entries 16q .. and 64+16q .. of
 // the 128 at k0), quantised; the four lanes that hold the block share its scale.
+// Magnitudes of bf16 numbers order like their low 15 bits, so the maximum runs on
+// pairs (16 and-s and 16 packed maxima); only a block with an infinity or a NaN
+// (a maximum of 0x7F80 or more) looks at its entries one by one.
 __device__ __forceinline__ i32x8 quant_fragment(const uint16_t* row, int64_t k0, int64_t k, bool vec,
                                                 int q, int* s) {
-    uint16_t v[4][8];
-    uint32_t m = 0u;
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t w[16];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        load8(row, k0 + 16 * q + 64 * (p >> 1) + 8 * (p & 1), k, vec, v[p]);
+        uint16_t v[8];
+        load8(row, k0 + 16 * q + 64 * (p >> 1) + 8 * (p & 1), k, vec, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(widen(v[p][i])));
+        for (int i = 0; i < 4; ++i) w[4 * p + i] = (uint32_t)v[2 * i] | ((uint32_t)v[2 * i + 1] << 16);
+    }
+    u16x2 m2 = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+    uint32_t m = max((uint32_t)m2[0], (uint32_t)m2[1]);
+    const bool special = m >= 0x7F80u;
+    if (__any(special)) {
+        if (special) {
+            m = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                // infinities become NaN, which the conversion keeps; zeros count as magnitudes
+                const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+                m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                if (lo >= 0x7F80u) w[i] |= 0x7FFFu;
+                if (hi >= 0x7F80u) w[i] |= 0x7FFF0000u;
+            }
+        }
     }
     m = max(m, (uint32_t)__shfl_xor(m, 16, 64));
     m = max(m, (uint32_t)__shfl_xor(m, 32, 64));
-    *s = scale_exponent(m);
+    *s = scale_exponent(m << 16);
     const float inv = inverse_scale(*s);
-    const u32x2 a = quant8(v[0], inv), b = quant8(v[1], inv), c = quant8(v[2], inv), d = quant8(v[3], inv);
-    return i32x8{(int)a.x, (int)a.y, (int)b.x, (int)b.y, (int)c.x, (int)c.y, (int)d.x, (int)d.y};
+    i32x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float a, b, c, d;
+        scale2(w[2 * i], inv, &a, &b);
+        scale2(w[2 * i + 1], inv, &c, &d);
+        r[i] = (int)pack4(a, b, c, d);
+    }
+    return r;
 }
 
-// Any shape: a wave owns 16 rows of A and 16 NT rows of X, operands straight
-// from memory.  QX: X is bf16 and quantised on the way.
-template <int NT, bool QX, class TY>
-__global__ __launch_bounds__(256) void spmm24_fp8_kernel(const void* __restrict__ X,
-                                                         const uint8_t* __restrict__ xs, int64_t n,
-                                                         int64_t ldx, bool xvec,
-                                                         const uint8_t* __restrict__ values,
-                                                         const uint32_t* __restrict__ meta,
-                                                         const uint8_t* __restrict__ scales, int64_t m,
-                                                         int64_t k, TY* __restrict__ Y, int64_t ldy,
-                                                         bool yvec) {
-    const int lane = threadIdx.x & 63, q = lane >> 4, l16 = lane & 15;
-    const int64_t mt = (m + 63) / 64;
-    const int64_t m0 = (blockIdx.x % mt) * 64 + 16 * (threadIdx.x >> 6);
-    const int64_t n0 = (blockIdx.x / mt) * (16 * NT);
-    if (m0 >= m) return;
-    const int64_t kb = (k + 127) / 128;
-    const int64_t row = min(m0 + l16, m - 1);
-    const uint8_t* arow = values + row * (kb * 64) + 16 * q;
-    const uint32_t* mrow = meta + row * (kb * 4) + q;
-    const uint8_t* srow = scales + (m0 >> 7) * kb;
-    int64_t col[NT];
+// Few tokens (n <= 16 NT): reading A bounds the product, so a workgroup owns 16 MT
+// rows of A and each of its eight waves a stretch of k, with the loads of kAhead
+// blocks in flight (stretches, not blocks in turn: the workgroup then reads whole rows
+// at a time, over all memory channels); the waves' sums meet in LDS, in wave order.  QX: X
+// is bf16 and quantised on the way.
+constexpr int kFewWaves = 8;
+
+template <int NT, int MT, bool QX, class TY>
+__global__ __launch_bounds__(64 * kFewWaves) void spmm24_fp8_few_kernel(
+    const void* __restrict__ X, const uint8_t* __restrict__ xs, int64_t n, int64_t ldx, bool xvec,
+    const uint8_t* __restrict__ values, const uint32_t* __restrict__ meta,
+    const uint8_t* __restrict__ scales, int64_t m, int64_t k, TY* __restrict__ Y, int64_t ldy,
+    bool yvec) {
+    constexpr int kAhead = QX ? 2 : NT * MT >= 4 ? 2 : 4;
+    __shared__ f32x4 sums[kFewWaves][MT * NT][64];
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t mt = (m + 16 * MT - 1) / (16 * MT);
+    const int64_t m0 = blockIdx.x % mt * (16 * MT), n0 = blockIdx.x / mt * (16 * NT);
+    const int kb = (int)((k + 127) / 128);
+    int64_t row[MT], col[NT];
+#pragma unroll
+    for (int a = 0; a < MT; ++a) row[a] = min(m0 + 16 * a + l16, m - 1);
 #pragma unroll
     for (int j = 0; j < NT; ++j) col[j] = min(n0 + 16 * j + l16, n - 1);
-    f32x4 acc[NT];
+    const uint8_t* srow = scales + (m0 >> 7) * kb;  // 16 MT rows lie in one block of 128
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t t = 0; t < kb; ++t) {
-        const i32x4 a = *reinterpret_cast<const i32x4*>(arow + 64 * t);
-        const int idx = (int)mrow[4 * t];
-        const int sa = srow[t];
+    for (int a = 0; a < MT; ++a)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            i32x8 b;
-            int sx;
-            if constexpr (QX) {
-                b = quant_fragment(static_cast<const uint16_t*>(X) + col[j] * ldx, 128 * t, k, xvec, q, &sx);
-                sx += 127;
-            } else {
-                const uint8_t* x = static_cast<const uint8_t*>(X) + col[j] * ldx + 128 * t + 16 * q;
-                b = join(*reinterpret_cast<const u32x4*>(x), *reinterpret_cast<const u32x4*>(x + 64));
-                sx = xs[t * n + col[j]];
+        for (int j = 0; j < NT; ++j) acc[a][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int tend = (int)((int64_t)kb * (wave + 1) / kFewWaves);
+    for (int t0 = (int)((int64_t)kb * wave / kFewWaves); t0 < tend; t0 += kAhead) {
+        i32x4 av[kAhead][MT];
+        int idx[kAhead][MT], sa[kAhead], sx[kAhead][NT];
+        i32x8 bv[kAhead][NT];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int t = min(t0 + u, tend - 1);  // behind the end: loaded, not used
+            sa[u] = srow[t];
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                av[u][a] = *reinterpret_cast<const i32x4*>(values + (row[a] * kb + t) * 64 + 16 * q);
+                idx[u][a] = (int)meta[(row[a] * kb + t) * 4 + q];
             }
-            f32x4 d = {0.f, 0.f, 0.f, 0.f};
-            d = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(a, b, d, idx, 0, 0);
-            const float f = scale_product(sa, sx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(d[i], f, acc[j][i]);
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (QX) {
+                    bv[u][j] = quant_fragment(static_cast<const uint16_t*>(X) + col[j] * ldx, 128 * (int64_t)t, k,
+                                              xvec, q, &sx[u][j]);
+                    sx[u][j] += 127;
+                } else {
+                    const uint8_t* x = static_cast<const uint8_t*>(X) + col[j] * ldx + 128 * (int64_t)t + 16 * q;
+                    bv[u][j] = join(*reinterpret_cast<const u32x4*>(x), *reinterpret_cast<const u32x4*>(x + 64));
+                    sx[u][j] = xs[t * n + col[j]];
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // all loads first
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (t0 + u >= tend) break;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float f = scale_product(sa[u], sx[u][j]);
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                    d = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(av[u][a], bv[u][j], d, idx[u][a], 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[a][j][i] = __builtin_fmaf(d[i], f, acc[a][j][i]);
+                }
+            }
         }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        if (n0 + 16 * j + l16 < n) store4(Y + col[j] * ldy, m0 + 4 * q, m, yvec, acc[j]);
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sums[wave][a * NT + j][lane] = acc[a][j];
+    __syncthreads();
+    for (int u = tid; u < MT * NT * 64; u += 64 * kFewWaves) {
+        f32x4 v = sums[0][u >> 6][u & 63];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += sums[w][u >> 6][u & 63];
+        const int l = u & 63, j = (u >> 6) % NT, a = (u >> 6) / NT;
+        const int64_t c = n0 + 16 * j + (l & 15);
+        if (c < n) store4(Y + c * ldy, m0 + 16 * a + 4 * (l >> 4), m, yvec, v);
+    }
 }
 
 // C = A B^T, any shape: a wave owns 16 columns of C (rows of B) and 64 rows.
@@ -452,21 +515,26 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
          hipStream_t stream) {
     TY* Y = static_cast<TY*>(Yv);
     const bool yvec = row4<TY>(Yv, ldy);
-    const int64_t mt = (m + 63) / 64;
-    if (bf16x) {
-        const bool xvec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && ldx % 8 == 0;
-        hipLaunchKernelGGL((spmm24_fp8_kernel<1, true, TY>), dim3((unsigned)mt), dim3(256), 0, stream, X,
-                           nullptr, n, ldx, xvec, values, meta, scales, m, k, Y, ldy, yvec);
-    } else if (n >= 128 && m >= 128 && ldx < kMaxRow && k < kMaxRow) {
+    if (!bf16x && n >= 128 && m >= 128 && ldx < kMaxRow && k < kMaxRow) {
         const int64_t blocks = ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
         hipLaunchKernelGGL((spmm24_fp8_large_kernel<TY>), dim3((unsigned)blocks), dim3(64 * kWaves), 0,
                            stream, static_cast<const uint8_t*>(X), xs, n, ldx, values, meta, scales, m, k,
                            Y, ldy, yvec);
-    } else {
-        hipLaunchKernelGGL((spmm24_fp8_kernel<4, false, TY>), dim3((unsigned)(mt * ((n + 63) / 64))),
-                           dim3(256), 0, stream, X, xs, n, ldx, true, values, meta, scales, m, k, Y, ldy,
-                           yvec);
+        return (int)hipGetLastError();
     }
+    const bool xvec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && ldx % 8 == 0;
+    const auto few = [&](auto kernel, int nt, int mt) {
+        const int64_t ny = (n + 16 * nt - 1) / (16 * nt), nx = (m + 16 * mt - 1) / (16 * mt);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(nx * ny)), dim3(64 * kFewWaves), 0, stream, X, xs, n,
+                           ldx, xvec, values, meta, scales, m, k, Y, ldy, yvec);
+    };
+    if (bf16x) few(spmm24_fp8_few_kernel<1, 1, true, TY>, 1, 1);
+    else if (n <= 16) few(spmm24_fp8_few_kernel<1, 1, false, TY>, 1, 1);
+    else if (n <= 32) few(spmm24_fp8_few_kernel<2, 1, false, TY>, 2, 1);
+    else if (n <= 48 && m < 8192) few(spmm24_fp8_few_kernel<3, 1, false, TY>, 3, 1);
+    else if (n <= 48) few(spmm24_fp8_few_kernel<3, 2, false, TY>, 3, 2);
+    else if (m < 8192) few(spmm24_fp8_few_kernel<4, 1, false, TY>, 4, 1);
+    else few(spmm24_fp8_few_kernel<4, 2, false, TY>, 4, 2);
     return (int)hipGetLastError();
 }
 
