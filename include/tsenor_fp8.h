@@ -106,8 +106,8 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
  *   logits = x R^T (products exact, sums in fp64); each token takes the `topk`
  *   largest (ties to the lowest index, NaN below every number) with weights
  *   softmax over those; y = sum_e w_e Down_e (silu(Gate_e x) * (Up_e x)).  The
- *   hidden vector is rounded to bf16 (2^-8 of each entry at most, the input
- *   type of the second product), y is rounded once.
+ *   hidden vector is held as the sum of two bf16 numbers (2^-16 of each entry
+ *   at most is lost), y is rounded once.
  *   X [n][ldx] bf16, 0 <= n <= 64;  router [experts][ldr] bf16;
  *   gate, up  batches of `experts` 2:4 operands [f][d];  down  [d][f];
  *   workspace device memory of at least tsenor_moe24_fp8_workspace(...) bytes,
@@ -115,7 +115,7 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
  *   Y [n][ldy] bf16;  ids int32 [n][topk] (largest logit first) and weights
  *            fp32 [n][topk]: the routing, or NULL.
  * Errors: _NULL, _PARAM (topk < 1, topk > experts, topk > 16, experts > 512), _SHAPE
- * (n < 0 or > 64, d, f <= 0, leading dimensions, alignment, workspace_bytes). */
+ * (n < 0 or > 64, d or f <= 0 or > 2^20, leading dimensions, alignment, workspace_bytes). */
 size_t tsenor_moe24_fp8_workspace(int64_t n, int64_t d, int64_t f, int64_t experts, int topk);
 int tsenor_moe24_fp8(const uint16_t* X, int64_t n, int64_t ldx, int64_t d, const uint16_t* router,
                      int64_t ldr, int64_t experts, int topk, const uint8_t* gate_values,

@@ -112,7 +112,7 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
 
 // The workspace's parts, each on a multiple of 256 bytes.
 struct MoeLayout {
-    size_t logits, xpad, hidden, ids, total;
+    size_t logits, xpad, hidden, ids, counts, chosen, lists, total;
 };
 static MoeLayout moe_layout(int64_t n, int64_t d, int64_t f, int64_t experts, int topk) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -120,13 +120,16 @@ static MoeLayout moe_layout(int64_t n, int64_t d, int64_t f, int64_t experts, in
     w.logits = 0;
     w.xpad = up((size_t)(n * experts) * sizeof(double));
     w.hidden = w.xpad + up((size_t)(n * blocks128(d) * 128) * 2);
-    w.ids = w.hidden + up((size_t)(n * topk * blocks128(f) * 128) * 2);
-    w.total = w.ids + up((size_t)(n * topk) * sizeof(int));
+    w.ids = w.hidden + up((size_t)(n * topk * blocks128(f) * 128) * 4);
+    w.counts = w.ids + up((size_t)(n * topk) * sizeof(int));
+    w.chosen = w.counts + up((size_t)experts * sizeof(int));
+    w.lists = w.chosen + up((size_t)experts * sizeof(int));
+    w.total = w.lists + up((size_t)experts * 64 * sizeof(int));
     return w;
 }
 static int moe_check(int64_t n, int64_t d, int64_t f, int64_t experts, int topk) {
     if (topk < 1 || topk > 16 || experts > 512 || topk > experts) return TSENOR_ERR_PARAM;
-    if (n < 0 || n > 64 || d <= 0 || f <= 0 || too_big(experts * 128, d + 128) ||
+    if (n < 0 || n > 64 || d <= 0 || f <= 0 || d > (1 << 20) || f > (1 << 20) || too_big(experts * 128, d + 128) ||
         too_big(experts * 128, f + 128) || too_big(experts * (d + 128), f + 128))
         return TSENOR_ERR_SHAPE;
     if (experts * ((f + 15) / 16) > kMaxGrid) return TSENOR_ERR_SHAPE;
@@ -181,6 +184,11 @@ int tsenor_moe24_fp8(const uint16_t* X, int64_t n, int64_t ldx, int64_t d, const
     job.xpad = reinterpret_cast<uint16_t*>(ws + w.xpad);
     job.hidden = reinterpret_cast<uint16_t*>(ws + w.hidden);
     job.ids = reinterpret_cast<int*>(ws + w.ids);
+    job.counts = reinterpret_cast<int*>(ws + w.counts);
+    job.chosen = reinterpret_cast<int*>(ws + w.chosen);
+    job.lists = reinterpret_cast<int*>(ws + w.lists);
+    job.xvec = !misaligned(X, 16) && ldx % 8 == 0;
+    job.rvec = !misaligned(router, 16) && ldr % 8 == 0;
     job.y = Y;
     job.ids_out = ids;
     job.weights_out = weights;

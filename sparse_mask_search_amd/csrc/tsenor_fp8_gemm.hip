@@ -528,13 +528,27 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
         hipLaunchKernelGGL(kernel, dim3((unsigned)(nx * ny)), dim3(64 * kFewWaves), 0, stream, X, xs, n,
                            ldx, xvec, values, meta, scales, m, k, Y, ldy, yvec);
     };
+    // A fragment of X touches 16 rows for each fragment of A that it meets, so with more tokens
+    // a workgroup takes more rows of A, as long as about 170 workgroups remain.  Measured (us)
+    // with 16 / 32 / 64 rows: 64 tokens, 11008 x 4096: 30.4 / 24.9 / 18.8; 16 tokens: 13.4 / 13.5 /
+    // 12.0; 1 token: 9.2 / 10.9 / 10.7; 64 tokens, 4096 x 11008: 27.8 / 31.9 / 42.0.
+    const int rows = m >= 64 * 160 ? 4 : m >= 32 * 160 ? 2 : 1;
     if (bf16x) few(spmm24_fp8_few_kernel<1, 1, true, TY>, 1, 1);
-    else if (n <= 16) few(spmm24_fp8_few_kernel<1, 1, false, TY>, 1, 1);
-    else if (n <= 32) few(spmm24_fp8_few_kernel<2, 1, false, TY>, 2, 1);
-    else if (n <= 48 && m < 8192) few(spmm24_fp8_few_kernel<3, 1, false, TY>, 3, 1);
-    else if (n <= 48) few(spmm24_fp8_few_kernel<3, 2, false, TY>, 3, 2);
-    else if (m < 8192) few(spmm24_fp8_few_kernel<4, 1, false, TY>, 4, 1);
-    else few(spmm24_fp8_few_kernel<4, 2, false, TY>, 4, 2);
+    else if (n <= 4) few(spmm24_fp8_few_kernel<1, 1, false, TY>, 1, 1);
+    else {
+        const auto pick = [&](auto one, auto two, auto four, int nt) {
+            if (rows == 4) few(four, nt, 4);
+            else if (rows == 2) few(two, nt, 2);
+            else few(one, nt, 1);
+        };
+#define FEW(NT) pick(spmm24_fp8_few_kernel<NT, 1, false, TY>, spmm24_fp8_few_kernel<NT, 2, false, TY>, \
+                     spmm24_fp8_few_kernel<NT, 4, false, TY>, NT)
+        if (n <= 16) FEW(1);
+        else if (n <= 32) FEW(2);
+        else if (n <= 48) FEW(3);
+        else FEW(4);
+#undef FEW
+    }
     return (int)hipGetLastError();
 }
 

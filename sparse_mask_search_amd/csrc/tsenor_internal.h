@@ -102,10 +102,12 @@ struct MoeJob {
     Operand24 gate, up, down;
     int64_t n, d, f, experts, ldx, ldr, ldy;
     int topk;
-    double* logits;    // workspace: [n][experts]
+    bool xvec, rvec;   // rows of x and router may be read 16 bytes at a time
+    double* logits;    // workspace: [experts][n]
     uint16_t* xpad;    // workspace: [n][d padded to 128]
-    uint16_t* hidden;  // workspace: [n topk][f padded to 128]
+    uint16_t* hidden;  // workspace: [2][n topk][f padded to 128]
     int* ids;          // workspace: [n topk]
+    int *counts, *chosen, *lists;  // workspace: [experts], [experts], [experts][64]
     uint16_t* y;
     int* ids_out;      // or nullptr
     float* weights_out;

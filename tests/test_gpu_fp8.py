@@ -553,8 +553,8 @@ def _moe_reference(xv, ids, wts, gate, up, down):
 
     Products of bf16 numbers are exact in fp32; a sum of t of them in any order is off by
     at most t * 2^-24 of its magnitudes (the matrix cores' adds are counted the same).  silu has slope
-    at most 1.1; exp, the division and two products: 2^-20.  The hidden entry is rounded
-    by 2^-8; the weights and the sum over experts: 2^-20."""
+    at most 1.1; exp, the division and two products: 2^-20.  The hidden entry loses at
+    most 2^-16; the weights and the sum over experts: 2^-20."""
     n, d = xv.shape
     f = gate.shape[1]
     y, bound = np.zeros((n, d)), np.zeros((n, d))
@@ -565,7 +565,7 @@ def _moe_reference(xv, ids, wts, gate, up, down):
             eg, eu = d * 2.0 ** -24 * (np.abs(gate[e]) @ np.abs(x)), d * 2.0 ** -24 * (np.abs(up[e]) @ np.abs(x))
             silu = g / (1 + np.exp(-g))
             h = silu * u
-            eh = 1.1 * eg * (np.abs(u) + eu) + np.abs(silu) * eu + (2.0 ** -20 + 2.0 ** -8) * np.abs(h)
+            eh = 1.1 * eg * (np.abs(u) + eu) + np.abs(silu) * eu + (2.0 ** -20 + 2.0 ** -16) * np.abs(h)
             a = np.abs(down[e])
             y[t] += w * (down[e] @ h)
             bound[t] += w * (a @ (1.01 * eh) + (f * 2.0 ** -24 + 2.0 ** -20) * (a @ np.abs(h)))
