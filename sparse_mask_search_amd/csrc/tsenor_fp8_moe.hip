@@ -34,7 +34,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kMaxTokens = 64, kMaxTop = 16, kMoeWaves = 8;
+constexpr int kMaxTokens = 64, kMaxTop = 16;
+constexpr int kHiddenWaves = 8, kOutputWaves = 16;
 
 // logits[e][t] in fp64 (products of bf16 numbers are exact in fp32).  A workgroup
 // per expert and four tokens, its four waves a quarter of d each; the workgroups
@@ -122,30 +123,40 @@ __host__ __device__ __forceinline__ bool compact(const MoeJob& a) {
     return a.n * a.topk < a.experts && a.n * a.experts <= kCompactLogits;
 }
 
-// hidden: one workgroup per (expert, 16 rows of gate and up).  Expert number j of the
+// hidden: one workgroup per (expert, 16 MT rows of gate and up).  Expert number j of the
 // grid (j-th chosen, or j itself) leaves its tokens' slots t * topk + rank in
 // lists[j], for the output.
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_hidden_kernel(MoeJob a) {
-    __shared__ f32x4 sums[kMoeWaves][2][64];
-    __shared__ double lds_logits[kCompactLogits];
+template <int MT>
+__global__ __launch_bounds__(64 * kHiddenWaves) void moe_hidden_kernel(MoeJob a) {
+    constexpr int kThreads = 64 * kHiddenWaves;
+    __shared__ union {
+        f32x4 sums[kHiddenWaves][2 * MT][64];
+        struct {
+            double logits[kCompactLogits];
+            uint16_t rank[kCompactLogits];
+        } all;
+    } lds;
     __shared__ uint32_t chosen[16];
-    __shared__ int ranks[kMoeWaves][kMaxTokens];
+    __shared__ int ranks[kHiddenWaves][kMaxTokens];
     __shared__ int slots[kMaxTokens];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t ft = (a.f + 15) / 16;
+    const int64_t ft = (a.f + 16 * MT - 1) / (16 * MT);
     const int j = (int)(blockIdx.x / ft), n = (int)a.n, experts = (int)a.experts;
-    const int64_t f0 = (blockIdx.x - j * ft) * 16;
-    int e = j;
+    const int64_t f0 = (blockIdx.x - j * ft) * (16 * MT);
+    int e = j, r = 0;
     if (compact(a)) {
         if (tid < 16) chosen[tid] = 0u;
-        for (int i = tid; i < n * experts; i += 64 * kMoeWaves) lds_logits[i] = a.logits[i];
+        for (int i = tid; i < n * experts; i += kThreads) lds.all.logits[i] = a.logits[i];
         __syncthreads();
-        for (int i = tid; i < n * experts; i += 64 * kMoeWaves) {
+        for (int i = tid; i < n * experts; i += kThreads) {
             const int c = i / n, t = i - c * n;
-            int r = 0;
-            for (int o = 0; o < experts; ++o) r += before(lds_logits[o * n + t], o, lds_logits[i], c) ? 1 : 0;
-            if (r < a.topk) atomicOr(&chosen[c >> 5], 1u << (c & 31));
+            const double mine = lds.all.logits[i];
+            int rank = 0;
+#pragma unroll 8
+            for (int o = 0; o < experts; ++o) rank += before(lds.all.logits[o * n + t], o, mine, c) ? 1 : 0;
+            lds.all.rank[i] = (uint16_t)rank;
+            if (rank < a.topk) atomicOr(&chosen[c >> 5], 1u << (c & 31));
         }
         __syncthreads();
         int left = j;
@@ -164,18 +175,22 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_hidden_kernel(MoeJob a) {
             if (f0 == 0 && tid == 0) a.counts[j] = 0;
             return;
         }
-    }
-    // rank of e for token `lane`; each wave compares with every eighth expert
-    int r = 0;
-    if (lane < n) {
-        const double le = a.logits[e * n + lane];
-        for (int o = wave; o < experts; o += kMoeWaves) r += before(a.logits[o * n + lane], o, le, e) ? 1 : 0;
-    }
-    ranks[wave][lane] = r;
-    __syncthreads();
-    r = 0;
+        e = __builtin_amdgcn_readfirstlane(e);
+        if (lane < n) r = lds.all.rank[e * n + lane];
+    } else {
+        // rank of e for token `lane`; each wave compares with every eighth expert
+        if (lane < n) {
+            const double le = a.logits[e * n + lane];
+#pragma unroll 8
+            for (int o = wave; o < experts; o += kHiddenWaves)
+                r += before(a.logits[o * n + lane], o, le, e) ? 1 : 0;
+        }
+        ranks[wave][lane] = r;
+        __syncthreads();
+        r = 0;
 #pragma unroll
-    for (int w = 0; w < kMoeWaves; ++w) r += ranks[w][lane];
+        for (int w = 0; w < kHiddenWaves; ++w) r += ranks[w][lane];
+    }
     const bool mine = lane < n && r < a.topk;
     const uint64_t who = __ballot(mine);  // the same in every wave
     const int count = __popcll(who);
@@ -198,25 +213,31 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_hidden_kernel(MoeJob a) {
     constexpr int kAhead = 2;
     const int kb = (int)((a.d + 127) / 128);
     const int64_t dp = kb * 128, fp = pad128(a.f);
-    const int64_t row = e * a.f + min(f0 + l16, a.f - 1);
-    const int64_t sb = (e * ((a.f + 127) / 128) + (f0 >> 7)) * kb;
-    const int tbegin = kb * wave / kMoeWaves, tend = kb * (wave + 1) / kMoeWaves;
+    int64_t row[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) row[m] = (e * a.f + min(f0 + 16 * m + l16, a.f - 1)) * kb;
+    const int64_t sb = (e * ((a.f + 127) / 128) + (f0 >> 7)) * kb;  // 16 MT rows lie in one block of 128
+    const int tbegin = kb * wave / kHiddenWaves, tend = kb * (wave + 1) / kHiddenWaves;
     for (int c0 = 0; c0 < count; c0 += 16) {
-        const int slot = slots[min(c0 + l16, count - 1)];
-        const uint16_t* x = a.xpad + (slot / a.topk) * dp;
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const uint16_t* x = a.xpad + (slots[min(c0 + l16, count - 1)] / a.topk) * dp;
+        f32x4 acc[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int t0 = tbegin; t0 < tend; t0 += kAhead) {
-            u32x4 v[kAhead][2];
-            uint32_t idx[kAhead][2];
+            u32x4 v[kAhead][MT][2];
+            uint32_t idx[kAhead][MT][2];
             int sc[kAhead][2];
             bf16x16 b[kAhead][2];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int t = min(t0 + u, tend - 1);
-                v[u][0] = *reinterpret_cast<const u32x4*>(a.gate.values + (row * kb + t) * 64 + 16 * q);
-                v[u][1] = *reinterpret_cast<const u32x4*>(a.up.values + (row * kb + t) * 64 + 16 * q);
-                idx[u][0] = a.gate.meta[(row * kb + t) * 4 + q];
-                idx[u][1] = a.up.meta[(row * kb + t) * 4 + q];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    v[u][m][0] = *reinterpret_cast<const u32x4*>(a.gate.values + (row[m] + t) * 64 + 16 * q);
+                    v[u][m][1] = *reinterpret_cast<const u32x4*>(a.up.values + (row[m] + t) * 64 + 16 * q);
+                    idx[u][m][0] = a.gate.meta[(row[m] + t) * 4 + q];
+                    idx[u][m][1] = a.up.meta[(row[m] + t) * 4 + q];
+                }
                 sc[u][0] = a.gate.scales[sb + t];
                 sc[u][1] = a.up.scales[sb + t];
                 load_block(x + 128 * t, q, b[u]);
@@ -226,40 +247,49 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_hidden_kernel(MoeJob a) {
             for (int u = 0; u < kAhead; ++u) {
                 if (t0 + u >= tend) break;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    bf16x8 av[2];
-                    widen_block(v[u][i], scale_value(sc[u][i]), av);
-                    acc[i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[0], b[u][0], acc[i], (int)idx[u][i], 0, 0);
-                    acc[i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[1], b[u][1], acc[i],
-                                                                       (int)(idx[u][i] >> 16), 0, 0);
-                }
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        bf16x8 av[2];
+                        widen_block(v[u][m][i], scale_value(sc[u][i]), av);
+                        acc[m][i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[0], b[u][0], acc[m][i],
+                                                                              (int)idx[u][m][i], 0, 0);
+                        acc[m][i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[1], b[u][1], acc[m][i],
+                                                                              (int)(idx[u][m][i] >> 16), 0, 0);
+                    }
             }
         }
-        sums[wave][0][lane] = acc[0];
-        sums[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (wave == 0 && c0 + l16 < count) {
-            f32x4 g = sums[0][0][lane], u = sums[0][1][lane];
 #pragma unroll
-            for (int w = 1; w < kMoeWaves; ++w) {
-                g += sums[w][0][lane];
-                u += sums[w][1][lane];
+        for (int m = 0; m < MT; ++m) {
+            lds.sums[wave][2 * m][lane] = acc[m][0];
+            lds.sums[wave][2 * m + 1][lane] = acc[m][1];
+        }
+        __syncthreads();
+        if (wave < MT && c0 + l16 < count) {
+            f32x4 g = lds.sums[0][2 * wave][lane], u = lds.sums[0][2 * wave + 1][lane];
+#pragma unroll
+            for (int w = 1; w < kHiddenWaves; ++w) {
+                g += lds.sums[w][2 * wave][lane];
+                u += lds.sums[w][2 * wave + 1][lane];
             }
-            uint16_t *hi = a.hidden + slot * fp, *lo = hi + a.n * a.topk * fp;
+            const int64_t f1 = f0 + 16 * wave;
+            uint16_t *hi = a.hidden + slots[c0 + l16] * fp, *lo = hi + a.n * a.topk * fp;
             u32x2 ph = {0u, 0u}, pl = {0u, 0u};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float h = f0 + 4 * q + i < a.f ? g[i] / (1.f + expf(-g[i])) * u[i] : 0.f;
+                const float h = f1 + 4 * q + i < a.f ? g[i] / (1.f + expf(-g[i])) * u[i] : 0.f;
                 const uint16_t top = to_bf16(h);
                 // what the first number leaves; nothing behind an infinity
                 const float rest = (top & 0x7F80u) == 0x7F80u ? 0.f : h - widen(top);
                 ph[i >> 1] |= (uint32_t)top << (16 * (i & 1));
                 pl[i >> 1] |= (uint32_t)to_bf16(rest) << (16 * (i & 1));
             }
-            *reinterpret_cast<u32x2*>(hi + f0 + 4 * q) = ph;
-            *reinterpret_cast<u32x2*>(lo + f0 + 4 * q) = pl;
-            if (f0 + 16 >= a.f)  // the last tile clears the padding behind it
-                for (int64_t i = f0 + 16 + q; i < fp; i += 4) hi[i] = lo[i] = 0;
+            if (f1 < fp) {
+                *reinterpret_cast<u32x2*>(hi + f1 + 4 * q) = ph;
+                *reinterpret_cast<u32x2*>(lo + f1 + 4 * q) = pl;
+            }
+            if (wave == MT - 1 && f1 + 16 >= a.f)  // the last tile clears the padding behind it
+                for (int64_t i = f1 + 16 + q; i < fp; i += 4) hi[i] = lo[i] = 0;
         }
         __syncthreads();
     }
@@ -281,9 +311,9 @@ __device__ __forceinline__ float weight_of(const MoeJob& a, int64_t t, int r) {
 // output: one workgroup per 16 rows of down.  The work is a sequence of blocks of 128
 // (expert after expert, 16 of its tokens after 16); each wave takes an equal stretch of
 // it and adds what an expert's tokens gain to its own partial sums.
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_output_kernel(MoeJob a, int groups) {
+__global__ __launch_bounds__(64 * kOutputWaves) void moe_output_kernel(MoeJob a, int groups) {
     constexpr int kMaxUnits = 512 + 64;  // (expert, 16 tokens) pairs: at most experts + n topk / 16
-    __shared__ float part[kMoeWaves][kMaxTokens][17];
+    __shared__ float part[kOutputWaves][kMaxTokens][17];
     __shared__ float wts[kMaxTokens * kMaxTop];
     __shared__ uint16_t unit_group[kMaxUnits], unit_expert[kMaxUnits], unit_slot[kMaxUnits][16];
     __shared__ uint8_t unit_first[kMaxUnits], unit_count[kMaxUnits];
@@ -314,8 +344,8 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_output_kernel(MoeJob a, in
         }
         if (lane == 0) total_units = base;
     }
-    for (int i = tid; i < kMoeWaves * kMaxTokens * 17; i += 64 * kMoeWaves) (&part[0][0][0])[i] = 0.f;
-    for (int i = tid; i < a.n * a.topk; i += 64 * kMoeWaves) {
+    for (int i = tid; i < kOutputWaves * kMaxTokens * 17; i += 64 * kOutputWaves) (&part[0][0][0])[i] = 0.f;
+    for (int i = tid; i < a.n * a.topk; i += 64 * kOutputWaves) {
         const float w = weight_of(a, i / a.topk, i % a.topk);
         wts[i] = w;
         if (blockIdx.x == 0) {
@@ -325,15 +355,15 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_output_kernel(MoeJob a, in
     }
     __syncthreads();
     const int total = __builtin_amdgcn_readfirstlane(total_units);
-    for (int i = tid; i < total * 16; i += 64 * kMoeWaves) {
+    for (int i = tid; i < total * 16; i += 64 * kOutputWaves) {
         const int u = i >> 4;
         unit_slot[u][i & 15] =
             (uint16_t)a.lists[unit_group[u] * kMaxTokens + unit_first[u] + min(i & 15, unit_count[u] - 1)];
     }
     __syncthreads();
-    constexpr int kAhead = 2;
+    constexpr int kAhead = 4;
     const int steps = total * kb;
-    const int begin = (int)((int64_t)steps * wave / kMoeWaves), end = (int)((int64_t)steps * (wave + 1) / kMoeWaves);
+    const int begin = (int)((int64_t)steps * wave / kOutputWaves), end = (int)((int64_t)steps * (wave + 1) / kOutputWaves);
     const int64_t dr = min(d0 + l16, a.d - 1);
     const int64_t drows = (a.d + 127) / 128;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
@@ -350,7 +380,7 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_output_kernel(MoeJob a, in
         u32x4 v[kAhead];
         uint32_t idx[kAhead];
         int sc[kAhead];
-        bf16x16 hi[kAhead][2], lo[kAhead][2];
+        const uint16_t* h[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int s = min(s0 + u, end - 1), unit = s / kb, t = s - unit * kb;
@@ -359,30 +389,40 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_output_kernel(MoeJob a, in
             v[u] = *reinterpret_cast<const u32x4*>(a.down.values + (row * kb + t) * 64 + 16 * q);
             idx[u] = a.down.meta[(row * kb + t) * 4 + q];
             sc[u] = a.down.scales[(e * drows + (d0 >> 7)) * kb + t];
-            load_block(a.hidden + slot * fp + 128 * t, q, hi[u]);
-            load_block(a.hidden + (a.n * a.topk + slot) * fp + 128 * t, q, lo[u]);
+            h[u] = a.hidden + slot * fp + 128 * t;
         }
-        __builtin_amdgcn_sched_barrier(0);  // all loads first
+        // the weights come from far, the hidden entries from L2: those follow in pairs
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int s = s0 + u;
-            if (s >= end) break;
-            bf16x8 av[2];
-            widen_block(v[u], scale_value(sc[u]), av);
+        for (int p = 0; p < kAhead; p += 2) {
+            bf16x16 hi[2][2], lo[2][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                y = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], hi[u][i], y, (int)(idx[u] >> (16 * i)), 0, 0);
-                y = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], lo[u][i], y, (int)(idx[u] >> (16 * i)), 0, 0);
+            for (int u = 0; u < 2; ++u) {
+                load_block(h[p + u], q, hi[u]);
+                load_block(h[p + u] + a.n * a.topk * fp, q, lo[u]);
             }
-            if (s + 1 == end || (s + 1) % kb == 0) flush(s / kb);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int s = s0 + p + u;
+                if (s >= end) break;
+                bf16x8 av[2];
+                widen_block(v[p + u], scale_value(sc[p + u]), av);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int x = (int)(idx[p + u] >> (16 * i));
+                    y = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], hi[u][i], y, x, 0, 0);
+                    y = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], lo[u][i], y, x, 0, 0);
+                }
+                if (s + 1 == end || (s + 1) % kb == 0) flush(s / kb);
+            }
         }
     }
     __syncthreads();
-    for (int i = tid; i < a.n * 16; i += 64 * kMoeWaves) {
+    for (int i = tid; i < a.n * 16; i += 64 * kOutputWaves) {
         const int t = i >> 4, r = i & 15;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kMoeWaves; ++w) sum += part[w][t][r];
+        for (int w = 0; w < kOutputWaves; ++w) sum += part[w][t][r];
         if (d0 + r < a.d) a.y[t * a.ldy + d0 + r] = to_bf16(sum);
     }
 }
@@ -395,12 +435,16 @@ int launch_moe24_fp8(const MoeJob& a, void* stream) {
     hipLaunchKernelGGL(moe_logits_kernel, dim3((unsigned)logit_blocks), dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
+    // 64 rows per workgroup where that leaves two workgroups per CU, else 32 or 16
     const int64_t groups = compact(a) ? a.n * a.topk : a.experts;
-    hipLaunchKernelGGL(moe_hidden_kernel, dim3((unsigned)(groups * ((a.f + 15) / 16))), dim3(64 * kMoeWaves), 0,
-                       s, a);
+    const auto tiles = [&](int rows) { return groups * ((a.f + rows - 1) / rows); };
+    const dim3 threads(64 * kHiddenWaves);
+    if (tiles(64) >= 512) hipLaunchKernelGGL(moe_hidden_kernel<4>, dim3((unsigned)tiles(64)), threads, 0, s, a);
+    else if (tiles(32) >= 512) hipLaunchKernelGGL(moe_hidden_kernel<2>, dim3((unsigned)tiles(32)), threads, 0, s, a);
+    else hipLaunchKernelGGL(moe_hidden_kernel<1>, dim3((unsigned)tiles(16)), threads, 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    hipLaunchKernelGGL(moe_output_kernel, dim3((unsigned)((a.d + 15) / 16)), dim3(64 * kMoeWaves), 0, s, a,
+    hipLaunchKernelGGL(moe_output_kernel, dim3((unsigned)((a.d + 15) / 16)), dim3(64 * kOutputWaves), 0, s, a,
                        (int)groups);
     return (int)hipGetLastError();
 }
