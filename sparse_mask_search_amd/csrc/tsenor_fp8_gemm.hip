@@ -238,17 +238,16 @@ __global__ __launch_bounds__(256) void gemm_fp8_kernel(const uint8_t* __restrict
     }
 }
 
-// ---- large products ----------------------------------------------------------
+// ---- tiled products -----------------------------------------------------------
 //
-// A workgroup of 8 waves owns 256 x 256 of the output, a wave 128 x 64 (4 x 2
-// tiles of 32 x 32), and walks k in blocks of 128.  Operands reach LDS by direct
-// loads (no register staging) into a ring of buffers.  Rows keep their 16-byte
-// chunks swizzled so that the 16 rows of one pass of a 16-byte LDS read hit 16
-// different bank groups: rows of 128 bytes keep chunk c at c ^ ((r >> 1) & 7), rows
-// of 64 bytes at c ^ ((r >> 2) & 3).  Rows behind an operand's end repeat its last
-// row; nothing of them is stored.
+// A workgroup of WM x WN waves owns TM x TN of the output, a wave (TM / WM) x
+// (TN / WN) in tiles of 32 x 32, and walks k in blocks of 128.  Operands reach LDS by
+// direct loads (no register staging) into a ring of R buffers filled R - 1 steps ahead.
+// Rows keep their 16-byte chunks swizzled so that the 16 rows of one pass of a 16-byte
+// LDS read hit 16 different bank groups: rows of 128 bytes keep chunk c at
+// c ^ ((r >> 1) & 7), rows of 64 bytes at c ^ ((r >> 2) & 3).  Rows behind an operand's
+// end repeat its last row; nothing of them is stored.
 
-constexpr int kTile = 256, kWaves = 8;
 constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside a tile fit 32 bits
 
 // Operand layout of the 32 x 32 x 64 instructions, lane l, h = l / 32 (probed like
@@ -257,45 +256,47 @@ constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside
 // rows 8 i0 + 4h + i1 in register 4 i0 + i1.  The dense instruction takes any order of
 // the entries that is the same for both operands.
 
-// Y = X A^T.  Three buffers filled two steps ahead: a step is 32 KB of X, 16 KB of
-// values, 4 KB of metadata and the scale bytes.
-template <class TY>
-__global__ __launch_bounds__(64 * kWaves) void spmm24_fp8_large_kernel(
+// Y = X A^T (A on the rows of the instruction).
+template <int TM, int TN, int WM, int WN, int R, class TY>
+__global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
     const uint8_t* __restrict__ X, const uint8_t* __restrict__ xs, int64_t n, int64_t ldx,
     const uint8_t* __restrict__ values, const uint32_t* __restrict__ meta,
     const uint8_t* __restrict__ scales, int64_t m, int64_t k, TY* __restrict__ Y, int64_t ldy,
     bool yvec) {
-    constexpr int QX = 4, QA = 2;  // direct loads of a wave per step: X, values and as many of metadata
+    constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
+    // direct loads of a wave per step: X, values and as many of metadata, one of scales
+    constexpr int QX = TN / 8 / W, QA = TM / 16 / W;
+    static_assert(QX * 8 * W == TN && QA * 16 * W == TM && TN / 64 < W, "tile");
     struct Buffer {
-        u32x4 x[kTile * 8];
-        u32x4 a[kTile * 4];
-        uint32_t meta[kTile * 4];
-        uint32_t scale[kTile + 64];  // of the X rows; of the two blocks of A rows (first two)
+        u32x4 x[TN * 8];
+        u32x4 a[TM * 4];
+        uint32_t meta[TM * 4];
+        uint32_t scale[TN + 64];  // of the X rows; of the blocks of A rows (the first two)
     };
-    __shared__ Buffer ring[3];
+    __shared__ Buffer ring[R];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, l32 = lane & 31;
+    const int wm = wave / WN, wn = wave % WN, h = lane >> 5, l32 = lane & 31;
     int64_t tm, tn;
-    tile_of(blockIdx.x, (m + kTile - 1) / kTile, (n + kTile - 1) / kTile, tm, tn);
-    const int64_t m0 = tm * kTile, n0 = tn * kTile, kb = (k + 127) / 128;
+    tile_of(blockIdx.x, (m + TM - 1) / TM, (n + TN - 1) / TN, tm, tn);
+    const int64_t m0 = tm * TM, n0 = tn * TN, kb = (k + 127) / 128;
     const int steps = (int)kb;
 
     // rows behind the operands' ends, from the tile's first row
-    const int xlast = (int)min(n - 1 - n0, (int64_t)kTile), alast = (int)min(m - 1 - m0, (int64_t)kTile);
+    const int xlast = (int)min(n - 1 - n0, (int64_t)TN), alast = (int)min(m - 1 - m0, (int64_t)TM);
     const uint8_t *xbase = X + n0 * ldx, *abase = values + m0 * (kb * 64);
     const uint8_t* mbase = reinterpret_cast<const uint8_t*>(meta + m0 * (kb * 4));
-    // waves 0 .. 3 bring 64 rows' scales each, the others all the same 64 (of A's blocks)
-    const bool xw = wave < 4;
+    // the first waves bring 64 X rows' scales each, the others all the same 64 (of A's blocks)
+    const bool xw = wave < TN / 64;
     const uint8_t* sbase = xw ? xs + n0 : scales + (m0 >> 7) * kb;
     const int64_t sstep = xw ? n : 1;
-    const int sdst = 64 * min(wave, 4);
+    const int sdst = 64 * min(wave, TN / 64);
 
-    f32x16 acc[4][2];
+    f32x16 acc[TA][TB];
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < TA; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < TB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
 
@@ -317,25 +318,26 @@ __global__ __launch_bounds__(64 * kWaves) void spmm24_fp8_large_kernel(
             dma16(abase + 64 * s, 64 * row + 16 * (c ^ ((r >> 2) & 3)), lds_offset(buf.a + 64 * (wave * QA + j)));
             dma4(mbase + 16 * s, 16 * row + 4 * c, lds_offset(buf.meta + 64 * (wave * QA + j)));
         }
-        const uint32_t so = xw ? min(64 * wave + l, xlast) : min(l & 1, (int)(((m - 1) >> 7) - (m0 >> 7))) * (uint32_t)kb;
+        const uint32_t so = xw ? min(64 * wave + l, xlast)
+                               : min(l & (TM / 128 > 1 ? 1 : 0), (int)(((m - 1) >> 7) - (m0 >> 7))) * (uint32_t)kb;
         dma_byte(sbase + s * sstep, so, lds_offset(buf.scale + sdst));
     };
     auto step = [&](int t, Buffer& buf, Buffer& next) {
-        // this step's loads have landed when at most the next step's are outstanding, and
-        // this wave's LDS reads of the step before are done; after the barrier that holds
-        // for all waves, so the buffer that step t + 2 fills is free
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(QX + 2 * QA + 1) : "memory");
+        // this step's loads have landed when at most the next R - 2 steps' are outstanding,
+        // and this wave's LDS reads of the step before are done; after the barrier that holds
+        // for all waves, so the buffer that step t + R - 1 fills is free
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((R - 2) * (QX + 2 * QA + 1)) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        issue(t + 2, next);
+        issue(t + R - 1, next);
         const int l = opaque(lane), lh = l >> 5, lr = l & 31;
-        float f[2];
-        i32x8 bv[2][2];
+        float f[TB];
+        i32x8 bv[2][TB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int r = 64 * wn + 32 * b + lr, sw = (lr >> 1) & 7;
-            f[b] = scale_product((int)buf.scale[r], (int)buf.scale[kTile + wm]);
+        for (int b = 0; b < TB; ++b) {
+            const int r = (TN / WN) * wn + 32 * b + lr, sw = (lr >> 1) & 7;
+            f[b] = scale_product((int)buf.scale[r], (int)buf.scale[TN + (TM > 128 ? wm : 0)]);
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc)
                 bv[kc][b] = join(buf.x[8 * r + ((4 * kc + lh) ^ sw)], buf.x[8 * r + ((4 * kc + 2 + lh) ^ sw)]);
@@ -347,7 +349,7 @@ __global__ __launch_bounds__(64 * kWaves) void spmm24_fp8_large_kernel(
         int idx[2][2];
         f32x16 d[2];
         auto read_a = [&](int a) {
-            const int r = 128 * wm + 32 * a + lr, sw = (lr >> 2) & 3;
+            const int r = (TM / WM) * wm + 32 * a + lr, sw = (lr >> 2) & 3;
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc) {
                 av[a & 1][kc] = __builtin_bit_cast(i32x4, buf.a[4 * r + ((2 * kc + lh) ^ sw)]);
@@ -355,104 +357,114 @@ __global__ __launch_bounds__(64 * kWaves) void spmm24_fp8_large_kernel(
             }
         };
         auto multiply = [&](int i) {
-            const int a = (i >> 1) & 1, b = i & 1;
+            const int a = (i / TB) & 1, b = i % TB;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) d[b][e] = 0.f;
-            d[b] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a][0], bv[0][b], d[b], idx[a][0], 0, 0);
-            d[b] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a][1], bv[1][b], d[b], idx[a][1], 0, 0);
+            for (int e = 0; e < 16; ++e) d[i & 1][e] = 0.f;
+            d[i & 1] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a][0], bv[0][b], d[i & 1], idx[a][0], 0, 0);
+            d[i & 1] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a][1], bv[1][b], d[i & 1], idx[a][1], 0, 0);
         };
         read_a(0);
         multiply(0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if ((i & 1) == 0 && i < 6) read_a((i >> 1) + 1);
-            if (i < 7) multiply(i + 1);
+        for (int i = 0; i < TA * TB; ++i) {
+            if (i % TB == 0 && i / TB + 1 < TA) read_a(i / TB + 1);
+            if (i + 1 < TA * TB) multiply(i + 1);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                acc[i >> 1][i & 1][e] = __builtin_fmaf(d[i & 1][e], f[i & 1], acc[i >> 1][i & 1][e]);
+                acc[i / TB][i % TB][e] = __builtin_fmaf(d[i & 1][e], f[i % TB], acc[i / TB][i % TB][e]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    issue(0, ring[0]);
-    issue(1, ring[1]);
+#pragma unroll
+    for (int t = 0; t < R - 1; ++t) issue(t, ring[t]);
     int cur = 0;
     for (int t = 0; t < steps; ++t) {
-        step(t, ring[cur], ring[cur == 0 ? 2 : cur - 1]);
-        cur = cur == 2 ? 0 : cur + 1;
+        step(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
+        cur = cur == R - 1 ? 0 : cur + 1;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const int64_t col = n0 + 64 * wn + 32 * b + l32;
+    for (int b = 0; b < TB; ++b) {
+        const int64_t col = n0 + (TN / WN) * wn + 32 * b + l32;
         if (col >= n) continue;
         TY* y = Y + col * ldy;
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < TA; ++a)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                store4(y, m0 + 128 * wm + 32 * a + 8 * i + 4 * h, m, yvec,
+                store4(y, m0 + (TM / WM) * wm + 32 * a + 8 * i + 4 * h, m, yvec,
                        f32x4{acc[a][b][4 * i], acc[a][b][4 * i + 1], acc[a][b][4 * i + 2], acc[a][b][4 * i + 3]});
     }
 }
 
-// C = A B^T.  Two buffers of 64 KB filled one step ahead; the scaled instruction
-// applies both operands' scales and adds in place.
-template <class TC>
-__global__ __launch_bounds__(64 * kWaves) void gemm_fp8_large_kernel(
+// C = A B^T (B on the rows of the instruction); the scaled instruction applies both
+// operands' scales and adds in place.
+template <int TM, int TN, int WM, int WN, int R, class TC>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tile_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t p,
     const uint8_t* __restrict__ B, const uint8_t* __restrict__ bs, int64_t qn, int64_t kb,
     const uint32_t* __restrict__ mask, TC* __restrict__ C, int64_t ldc, bool cvec) {
-    constexpr int Q = 4;
+    constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
+    constexpr int QB = TM / 8 / W, QA = TN / 8 / W;
+    static_assert(QB * 8 * W == TM && QA * 8 * W == TN && (TM + TN) / 64 <= W, "tile");
     struct Buffer {
-        u32x4 b[kTile * 8];  // rows of B (columns of C)
-        u32x4 a[kTile * 8];
-        uint32_t scale[2 * kTile];
+        u32x4 b[TM * 8];  // rows of B (columns of C)
+        u32x4 a[TN * 8];
+        uint32_t scale[TM + TN];
     };
-    __shared__ Buffer ring[2];
+    __shared__ Buffer ring[R];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, l32 = lane & 31;
+    const int wm = wave / WN, wn = wave % WN, h = lane >> 5, l32 = lane & 31;
     int64_t tm, tn;
-    tile_of(blockIdx.x, (qn + kTile - 1) / kTile, (p + kTile - 1) / kTile, tm, tn);
-    const int64_t m0 = tm * kTile, n0 = tn * kTile;
+    tile_of(blockIdx.x, (qn + TM - 1) / TM, (p + TN - 1) / TN, tm, tn);
+    const int64_t m0 = tm * TM, n0 = tn * TN;
     const int steps = (int)kb;
-    const int blast = (int)min(qn - 1 - m0, (int64_t)kTile), alast = (int)min(p - 1 - n0, (int64_t)kTile);
+    const int blast = (int)min(qn - 1 - m0, (int64_t)TM), alast = (int)min(p - 1 - n0, (int64_t)TN);
     const uint8_t *bbase = B + m0 * (kb * 128), *abase = A + n0 * (kb * 128);
-    const bool bw = wave < 4;
+    // each wave brings 64 rows' scales, of B first (waves left over: of the last 64 again)
+    const int sgroup = min(wave, (TM + TN) / 64 - 1);
+    const bool bw = sgroup < TM / 64;
     const uint8_t* sbase = bw ? bs + m0 : as + n0;
     const int64_t sstep = bw ? qn : p;
+    const int srow = 64 * (bw ? sgroup : sgroup - TM / 64);
 
-    f32x16 acc[4][2];
+    f32x16 acc[TA][TB];
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < TA; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < TB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
 
     auto issue = [&](int t, Buffer& buf) {
+        const int64_t s = t < steps ? t : steps - 1;
         const int l = opaque(lane);
         const uint32_t ld = (uint32_t)(kb * 128);
 #pragma unroll
-        for (int j = 0; j < Q; ++j) {
-            const int r = 8 * (wave * Q + j) + (l >> 3), c = 16 * ((l & 7) ^ ((r >> 1) & 7));
-            dma16(bbase + 128 * (int64_t)t, __umul24(min(r, blast), ld) + c, lds_offset(buf.b + 64 * (wave * Q + j)));
-            dma16(abase + 128 * (int64_t)t, __umul24(min(r, alast), ld) + c, lds_offset(buf.a + 64 * (wave * Q + j)));
+        for (int j = 0; j < QB; ++j) {
+            const int r = 8 * (wave * QB + j) + (l >> 3), c = 16 * ((l & 7) ^ ((r >> 1) & 7));
+            dma16(bbase + 128 * s, __umul24(min(r, blast), ld) + c, lds_offset(buf.b + 64 * (wave * QB + j)));
         }
-        dma_byte(sbase + t * sstep, min(64 * (wave & 3) + l, bw ? blast : alast), lds_offset(buf.scale + 64 * wave));
+#pragma unroll
+        for (int j = 0; j < QA; ++j) {
+            const int r = 8 * (wave * QA + j) + (l >> 3), c = 16 * ((l & 7) ^ ((r >> 1) & 7));
+            dma16(abase + 128 * s, __umul24(min(r, alast), ld) + c, lds_offset(buf.a + 64 * (wave * QA + j)));
+        }
+        dma_byte(sbase + s * sstep, min(srow + l, bw ? blast : alast), lds_offset(buf.scale + 64 * sgroup));
     };
-    auto step = [&](int t, Buffer& buf, Buffer& next) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    auto step = [&](int t, Buffer& buf, Buffer& next) {  // as in the product above
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((R - 2) * (QB + QA + 1)) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        if (t + 1 < steps) issue(t + 1, next);
-        int sn[2];
-        i32x8 nv[2][2];
+        issue(t + R - 1, next);
+        int sn[TB];
+        i32x8 nv[2][TB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int r = 64 * wn + 32 * b + l32, sw = (r >> 1) & 7;
-            sn[b] = (int)buf.scale[kTile + r];
+        for (int b = 0; b < TB; ++b) {
+            const int r = (TN / WN) * wn + 32 * b + l32, sw = (l32 >> 1) & 7;
+            sn[b] = (int)buf.scale[TM + r];
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc)
                 nv[kc][b] = join(buf.a[8 * r + ((4 * kc + h) ^ sw)], buf.a[8 * r + ((4 * kc + 2 + h) ^ sw)]);
@@ -460,7 +472,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_large_kernel(
         i32x8 mv[2][2];
         int sm[2];
         auto read_b = [&](int a) {
-            const int r = 128 * wm + 32 * a + l32, sw = (r >> 1) & 7;
+            const int r = (TM / WM) * wm + 32 * a + l32, sw = (l32 >> 1) & 7;
             sm[a & 1] = (int)buf.scale[r];
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc)
@@ -468,28 +480,35 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_large_kernel(
         };
         read_b(0);
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            if (a < 3) read_b(a + 1);
+        for (int a = 0; a < TA; ++a) {
+            if (a + 1 < TA) read_b(a + 1);
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc)
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < TB; ++b)
                     acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                         mv[a & 1][kc], nv[kc][b], acc[a][b], 0, 0, 0, sm[a & 1], 0, sn[b]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if (steps > 0) issue(0, ring[0]);
-    for (int t = 0; t < steps; ++t) step(t, ring[t & 1], ring[(t & 1) ^ 1]);
+    if (steps > 0)
+#pragma unroll
+        for (int t = 0; t < R - 1; ++t) issue(t, ring[t]);
+    int cur = 0;
+    for (int t = 0; t < steps; ++t) {
+        step(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
+        cur = cur == R - 1 ? 0 : cur + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     const int64_t wpr = (qn + 31) / 32;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const int64_t col = n0 + 64 * wn + 32 * b + l32;
+    for (int b = 0; b < TB; ++b) {
+        const int64_t col = n0 + (TN / WN) * wn + 32 * b + l32;
         if (col >= p) continue;
         TC* c = C + col * ldc;
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const int64_t c0 = m0 + 128 * wm + 32 * a;  // a multiple of 32: one mask word
+        for (int a = 0; a < TA; ++a) {
+            const int64_t c0 = m0 + (TM / WM) * wm + 32 * a;  // a multiple of 32: one mask word
             if (c0 >= qn) continue;
             const uint32_t keep = mask != nullptr ? mask[col * wpr + (c0 >> 5)] : 0xFFFFFFFFu;
 #pragma unroll
@@ -504,6 +523,20 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_fp8_large_kernel(
     }
 }
 
+int64_t tiles(int64_t a, int64_t b, int64_t ta, int64_t tb) { return ((a + ta - 1) / ta) * ((b + tb - 1) / tb); }
+
+// The largest tile that leaves every CU a workgroup (256 x 256), or two of them (smaller
+// tiles leave room for several on a CU): 0: 256 x 256, 1: 128 x 128, 2: 128 x 64, 3: 64 x 64.
+// Measured (us, the product alone) for 0 / 1 / 2 / 3: 4096 x 11008 x 4096: 240 / 300 / 374 / 418;
+// 2048 x 4096 x 4096: 64 / 55 / 65 / 75; 1000 x 4096 x 4096: 61 / 37 / 35 / 42; 300 x 4096 x 4096:
+// 60 / 33 / 25 / 22; dense 4096 x 11008 over 4096: 224 / 236 / 314 / 345, 1024 x 1024 over 1001: 23 /
+// 11.4 / 9.1 / 7.5.
+int pick_tile(int64_t a, int64_t b) {
+    if (tiles(a, b, 256, 256) >= 256) return 0;
+    if (tiles(a, b, 128, 128) >= 512) return 1;
+    return tiles(a, b, 128, 64) >= 512 ? 2 : 3;
+}
+
 template <class TY>
 bool row4(const void* y, int64_t ld) {
     return (reinterpret_cast<uintptr_t>(y) % (4 * sizeof(TY))) == 0 && ld % 4 == 0;
@@ -515,11 +548,18 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
          hipStream_t stream) {
     TY* Y = static_cast<TY*>(Yv);
     const bool yvec = row4<TY>(Yv, ldy);
-    if (!bf16x && n >= 128 && m >= 128 && ldx < kMaxRow && k < kMaxRow) {
-        const int64_t blocks = ((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
-        hipLaunchKernelGGL((spmm24_fp8_large_kernel<TY>), dim3((unsigned)blocks), dim3(64 * kWaves), 0,
-                           stream, static_cast<const uint8_t*>(X), xs, n, ldx, values, meta, scales, m, k,
-                           Y, ldy, yvec);
+    const bool tiled = !bf16x && n > 64 && m >= 64 && ldx < kMaxRow && k < kMaxRow;
+    if (tiled) {
+        const auto go = [&](auto kernel, int tm, int tn, int waves) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)tiles(m, n, tm, tn)), dim3(64 * waves), 0, stream,
+                               static_cast<const uint8_t*>(X), xs, n, ldx, values, meta, scales, m, k, Y, ldy, yvec);
+        };
+        switch (pick_tile(m, n)) {
+            case 0: go(spmm24_fp8_tile_kernel<256, 256, 2, 4, 3, TY>, 256, 256, 8); break;
+            case 1: go(spmm24_fp8_tile_kernel<128, 128, 2, 2, 2, TY>, 128, 128, 4); break;
+            case 2: go(spmm24_fp8_tile_kernel<128, 64, 2, 2, 3, TY>, 128, 64, 4); break;
+            default: go(spmm24_fp8_tile_kernel<64, 64, 2, 2, 3, TY>, 64, 64, 4); break;
+        }
         return (int)hipGetLastError();
     }
     const bool xvec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && ldx % 8 == 0;
@@ -555,11 +595,17 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
 template <class TC>
 int gemm(const uint8_t* A, const uint8_t* as, int64_t p, const uint8_t* B, const uint8_t* bs,
          int64_t q, int64_t k, const uint32_t* mask, void* C, int64_t ldc, hipStream_t stream) {
-    if (p >= 128 && q >= 128 && k < kMaxRow) {
-        const int64_t tiles = ((q + kTile - 1) / kTile) * ((p + kTile - 1) / kTile);
-        hipLaunchKernelGGL((gemm_fp8_large_kernel<TC>), dim3((unsigned)tiles), dim3(64 * kWaves), 0, stream,
-                           A, as, p, B, bs, q, (k + 127) / 128, mask, static_cast<TC*>(C), ldc,
-                           row4<TC>(C, ldc));
+    if (p >= 64 && q >= 64 && k < kMaxRow) {
+        const auto go = [&](auto kernel, int tm, int tn, int waves) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)tiles(q, p, tm, tn)), dim3(64 * waves), 0, stream, A, as, p, B,
+                               bs, q, (k + 127) / 128, mask, static_cast<TC*>(C), ldc, row4<TC>(C, ldc));
+        };
+        switch (pick_tile(q, p)) {
+            case 0: go(gemm_fp8_tile_kernel<256, 256, 2, 4, 2, TC>, 256, 256, 8); break;
+            case 1: go(gemm_fp8_tile_kernel<128, 128, 2, 2, 2, TC>, 128, 128, 4); break;
+            case 2: go(gemm_fp8_tile_kernel<128, 64, 2, 2, 3, TC>, 128, 64, 4); break;
+            default: go(gemm_fp8_tile_kernel<64, 64, 2, 2, 3, TC>, 64, 64, 4); break;
+        }
         return (int)hipGetLastError();
     }
     const int64_t blocks = ((q + 63) / 64) * ((p + 63) / 64);
