@@ -439,7 +439,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tile_kernel(
 
     auto issue = [&](int t, Buffer& buf) {
         const int64_t s = t < steps ? t : steps - 1;
-        const int l = opaque(lane);
+        const int l = lane;
         const uint32_t ld = (uint32_t)(kb * 128);
 #pragma unroll
         for (int j = 0; j < QB; ++j) {
@@ -500,6 +500,170 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tile_kernel(
         cur = cur == R - 1 ? 0 : cur + 1;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int64_t wpr = (qn + 31) / 32;
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+        const int64_t col = n0 + (TN / WN) * wn + 32 * b + l32;
+        if (col >= p) continue;
+        TC* c = C + col * ldc;
+#pragma unroll
+        for (int a = 0; a < TA; ++a) {
+            const int64_t c0 = m0 + (TM / WM) * wm + 32 * a;  // a multiple of 32: one mask word
+            if (c0 >= qn) continue;
+            const uint32_t keep = mask != nullptr ? mask[col * wpr + (c0 >> 5)] : 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = (keep >> (8 * i + 4 * h + e)) & 1u ? acc[a][b][4 * i + e] : 0.f;
+                store4(c, c0 + 8 * i + 4 * h, qn, cvec, v);
+            }
+        }
+    }
+}
+
+// The same product for many 256 x 256 tiles.  A step is half a block (64 entries): rows of
+// 64 bytes, four chunks kept at c ^ ((r >> 2) & 3), which leaves room for four buffers.
+// The operands of the next step's first instructions are read while this step's last ones
+// run, so the barrier that publishes the next buffer stands in the middle of a step, where
+// no wave waits for LDS.  The matrix cores are busy 64% of the time (51% with whole blocks
+// per step and the barrier at its start); the clock falls from 1.94 to 1.76 GHz with it, so
+// that the power limit takes back most of the gain: 8192^3 504 -> 475 us, 2.3 PFLOP/s.
+// Four waves of 128 x 128 measured 490 us; smaller tiles are slower in this form (128 x 128
+// at 8192 x 4096 x 8192: 352 us against 290).
+template <int TM, int TN, int WM, int WN, int R, class TC>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_wide_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t p,
+    const uint8_t* __restrict__ B, const uint8_t* __restrict__ bs, int64_t qn, int64_t kb,
+    const uint32_t* __restrict__ mask, TC* __restrict__ C, int64_t ldc, bool cvec) {
+    constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
+    // direct loads of a wave per step: of B, of A, and of 64 rows' scales
+    constexpr int QB = TM / 16 / W, QA = TN / 16 / W, G = (TM + TN) / 64, QS = (G + W - 1) / W;
+    static_assert(QB * 16 * W == TM && QA * 16 * W == TN && R >= 3, "tile");
+    struct Buffer {
+        u32x4 b[TM * 4];  // rows of B (columns of C)
+        u32x4 a[TN * 4];
+        uint32_t scale[TM + TN];
+    };
+    __shared__ Buffer ring[R];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, h = lane >> 5, l32 = lane & 31;
+    int64_t tm, tn;
+    tile_of(blockIdx.x, (qn + TM - 1) / TM, (p + TN - 1) / TN, tm, tn);
+    const int64_t m0 = tm * TM, n0 = tn * TN;
+    const int steps = 2 * (int)kb;
+    const int blast = (int)min(qn - 1 - m0, (int64_t)TM), alast = (int)min(p - 1 - n0, (int64_t)TN);
+    const uint8_t *bbase = B + m0 * (kb * 128), *abase = A + n0 * (kb * 128);
+    f32x16 acc[TA][TB];
+#pragma unroll
+    for (int a = 0; a < TA; ++a)
+#pragma unroll
+        for (int b = 0; b < TB; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+
+    // load number j of step t into its buffer (behind the last step: the last step again,
+    // into a buffer that nobody reads any more)
+    constexpr int kLoads = QB + QA + QS, kLate = TA > 1 ? kLoads / 2 : 0;
+    auto load = [&](int j, int t, Buffer& buf) {
+        const int64_t s = t < steps ? t : steps - 1;
+        const int l = lane;
+        const uint32_t ld = (uint32_t)(kb * 128);
+        if (j < QB) {
+            const int r = 16 * (wave * QB + j) + (l >> 2), c = 16 * ((l & 3) ^ ((r >> 2) & 3));
+            dma16(bbase + 64 * s, __umul24(min(r, blast), ld) + c, lds_offset(buf.b + 64 * (wave * QB + j)));
+        } else if (j < QB + QA) {
+            const int i = wave * QA + j - QB, r = 16 * i + (l >> 2), c = 16 * ((l & 3) ^ ((r >> 2) & 3));
+            dma16(abase + 64 * s, __umul24(min(r, alast), ld) + c, lds_offset(buf.a + 64 * i));
+        } else {
+            // 64 rows' scales, of B first (waves left over: of the last 64 again)
+            const int g = min(wave + (j - QB - QA) * W, G - 1);
+            const bool ofb = g < TM / 64;
+            const int64_t rows = ofb ? qn : p;
+            dma_byte((ofb ? bs + m0 : as + n0) + (s >> 1) * rows,
+                     min(64 * (ofb ? g : g - TM / 64) + l, ofb ? blast : alast), lds_offset(buf.scale + 64 * g));
+        }
+    };
+    i32x8 nv[2][TB], mv[2];
+    int sn[2][TB], sm[2];
+    auto read_b = [&](int a, const Buffer& buf) {  // 32 rows of B into the set a & 1
+        const int l = lane, r = (TM / WM) * wm + 32 * a + (l & 31), c = (l >> 5) ^ ((l >> 2) & 3);
+        sm[a & 1] = (int)buf.scale[r];
+        mv[a & 1] = join(buf.b[4 * r + c], buf.b[4 * r + (c ^ 2)]);
+    };
+    auto read_a = [&](int set, const Buffer& buf) {
+        const int l = lane, c = (l >> 5) ^ ((l >> 2) & 3);
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+            const int r = (TN / WN) * wn + 32 * b + (l & 31);
+            sn[set][b] = (int)buf.scale[TM + r];
+            nv[set][b] = join(buf.a[4 * r + c], buf.a[4 * r + (c ^ 2)]);
+        }
+    };
+    // Step t, whose first operands are in registers (set t & 1).  The loads of step
+    // t + R - 1 go out one by one between the matrix instructions (all at once they would
+    // stall every wave on the address unit): the first ones after the barrier, the last
+    // kLate in the first half of the next step.
+    auto step = [&](int t, int set, const Buffer& buf, const Buffer& next, Buffer& early, Buffer& late) {
+#pragma unroll
+        for (int a = 0; a < TA; ++a) {
+            if (a == TA / 2) {
+                // the next step's loads have landed, and every wave is past the step before
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 3) * kLoads) : "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (a + 1 < TA) {
+                read_b(a + 1, buf);
+            } else {
+                read_a(set ^ 1, next);
+                if (TA > 1) read_b(0, next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    mv[a & 1], nv[set][b], acc[a][b], 0, 0, 0, sm[a & 1], 0, sn[set][b]);
+                __builtin_amdgcn_sched_barrier(0);
+                constexpr int kSlots = TA > 1 ? TA / 2 * TB : TB;  // of a half step
+                const int slot = (a >= TA / 2 ? a - TA / 2 : a) * TB + b;
+                if (a >= TA / 2) {
+#pragma unroll
+                    for (int j = slot; j < kLoads - kLate; j += kSlots) load(j, t + R - 1, early);
+                } else {
+#pragma unroll
+                    for (int j = slot; j < kLate; j += kSlots) load(kLoads - kLate + j, t + R - 2, late);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (TA == 1) read_b(0, next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if (steps > 0) {
+#pragma unroll
+        for (int t = 0; t < R - 1; ++t)
+#pragma unroll
+            for (int j = 0; j < (t == R - 2 ? kLoads - kLate : kLoads); ++j) load(j, t, ring[t]);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 2) * kLoads - kLate) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read_a(0, ring[0]);
+        read_b(0, ring[0]);
+        const auto inc = [](int v) { return v == R - 1 ? 0 : v + 1; };
+        const auto dec = [](int v) { return v == 0 ? R - 1 : v - 1; };
+        int cur = 0;
+        for (int t = 0; t < steps; t += 2) {
+            const int one = inc(cur), two = inc(one), last = dec(cur);
+            step(t, 0, ring[cur], ring[one], ring[last], ring[dec(last)]);
+            step(t + 1, 1, ring[one], ring[two], ring[cur], ring[last]);
+            cur = two;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
     const int64_t wpr = (qn + 31) / 32;
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
@@ -601,7 +765,7 @@ int gemm(const uint8_t* A, const uint8_t* as, int64_t p, const uint8_t* B, const
                                bs, q, (k + 127) / 128, mask, static_cast<TC*>(C), ldc, row4<TC>(C, ldc));
         };
         switch (pick_tile(q, p)) {
-            case 0: go(gemm_fp8_tile_kernel<256, 256, 2, 4, 2, TC>, 256, 256, 8); break;
+            case 0: go(gemm_fp8_wide_kernel<256, 256, 2, 4, 4, TC>, 256, 256, 8); break;
             case 1: go(gemm_fp8_tile_kernel<128, 128, 2, 2, 2, TC>, 128, 128, 4); break;
             case 2: go(gemm_fp8_tile_kernel<128, 64, 2, 2, 3, TC>, 128, 64, 4); break;
             default: go(gemm_fp8_tile_kernel<64, 64, 2, 2, 3, TC>, 64, 64, 4); break;
