@@ -112,7 +112,7 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
 
 // The workspace's parts, each on a multiple of 256 bytes.
 struct MoeLayout {
-    size_t logits, xpad, hidden, ids, counts, chosen, lists, total;
+    size_t logits, xpad, hidden, weights, counts, chosen, lists, gains, total;
 };
 static MoeLayout moe_layout(int64_t n, int64_t d, int64_t f, int64_t experts, int topk) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -120,11 +120,12 @@ static MoeLayout moe_layout(int64_t n, int64_t d, int64_t f, int64_t experts, in
     w.logits = 0;
     w.xpad = up((size_t)(n * experts) * sizeof(double));
     w.hidden = w.xpad + up((size_t)(n * blocks128(d) * 128) * 2);
-    w.ids = w.hidden + up((size_t)(n * topk * blocks128(f) * 128) * 4);
-    w.counts = w.ids + up((size_t)(n * topk) * sizeof(int));
+    w.weights = w.hidden + up((size_t)(n * topk * blocks128(f) * 128) * 4);
+    w.counts = w.weights + up((size_t)(n * topk) * sizeof(float));
     w.chosen = w.counts + up((size_t)experts * sizeof(int));
     w.lists = w.chosen + up((size_t)experts * sizeof(int));
-    w.total = w.lists + up((size_t)experts * 64 * sizeof(int));
+    w.gains = w.lists + up((size_t)experts * 64 * sizeof(int));
+    w.total = w.gains + up((size_t)(n * topk * ((d + 3) / 4 * 4)) * sizeof(float));
     return w;
 }
 static int moe_check(int64_t n, int64_t d, int64_t f, int64_t experts, int topk) {
@@ -183,10 +184,11 @@ int tsenor_moe24_fp8(const uint16_t* X, int64_t n, int64_t ldx, int64_t d, const
     job.logits = reinterpret_cast<double*>(ws + w.logits);
     job.xpad = reinterpret_cast<uint16_t*>(ws + w.xpad);
     job.hidden = reinterpret_cast<uint16_t*>(ws + w.hidden);
-    job.ids = reinterpret_cast<int*>(ws + w.ids);
+    job.weights = reinterpret_cast<float*>(ws + w.weights);
     job.counts = reinterpret_cast<int*>(ws + w.counts);
     job.chosen = reinterpret_cast<int*>(ws + w.chosen);
     job.lists = reinterpret_cast<int*>(ws + w.lists);
+    job.gains = reinterpret_cast<float*>(ws + w.gains);
     job.xvec = !misaligned(X, 16) && ldx % 8 == 0;
     job.rvec = !misaligned(router, 16) && ldr % 8 == 0;
     job.y = Y;

@@ -106,8 +106,9 @@ struct MoeJob {
     double* logits;    // workspace: [experts][n]
     uint16_t* xpad;    // workspace: [n][d padded to 128]
     uint16_t* hidden;  // workspace: [2][n topk][f padded to 128]
-    int* ids;          // workspace: [n topk]
+    float* weights;    // workspace: [n topk]
     int *counts, *chosen, *lists;  // workspace: [experts], [experts], [experts][64]
+    float* gains;      // workspace: [n topk][d padded to 4]
     uint16_t* y;
     int* ids_out;      // or nullptr
     float* weights_out;
