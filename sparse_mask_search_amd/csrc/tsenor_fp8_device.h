@@ -153,6 +153,22 @@ __device__ __forceinline__ int opaque(int v) {
     return v;
 }
 
+// Metadata of four blocks of a row at once.  A block's four words are for the four lane
+// groups q = lane / 16; read one by one, a load brings 16 bytes of each of 16 rows and costs
+// the address unit as much as one that brings 64.  So lane group g reads all four words of
+// block g, and a 4 x 4 transposition across the lane groups hands each its own: word[u] is
+// then this lane group's word of block u.
+__device__ __forceinline__ void words_of_blocks(const u32x4 mine, uint32_t word[4]) {
+    const u32x2 a = __builtin_amdgcn_permlane32_swap(mine[0], mine[2], false, false);
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(mine[1], mine[3], false, false);
+    const u32x2 c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const u32x2 d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    word[0] = c[0];
+    word[1] = c[1];
+    word[2] = d[0];
+    word[3] = d[1];
+}
+
 // Maximum over the 16 lanes of a row of lanes.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
 #pragma unroll

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void spmm24_fp8_few_kernel(
     const uint8_t* __restrict__ values, const uint32_t* __restrict__ meta,
     const uint8_t* __restrict__ scales, int64_t m, int64_t k, TY* __restrict__ Y, int64_t ldy,
     bool yvec) {
-    constexpr int kAhead = QX ? 2 : NT * MT >= 4 ? 2 : 4;
+    constexpr int kAhead = QX ? 2 : NT * MT >= 4 ? 2 : 4;  // divides 4
     __shared__ f32x4 sums[kFewWaves][MT * NT][64];
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -133,45 +133,55 @@ __global__ __launch_bounds__(64 * kFewWaves) void spmm24_fp8_few_kernel(
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[a][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int tend = (int)((int64_t)kb * (wave + 1) / kFewWaves);
-    for (int t0 = (int)((int64_t)kb * wave / kFewWaves); t0 < tend; t0 += kAhead) {
-        i32x4 av[kAhead][MT];
-        int idx[kAhead][MT], sa[kAhead], sx[kAhead][NT];
-        i32x8 bv[kAhead][NT];
+    for (int t0 = (int)((int64_t)kb * wave / kFewWaves); t0 < tend; t0 += 4) {
+        u32x4 own[MT];
+        uint32_t idx[MT][4];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int t = min(t0 + u, tend - 1);  // behind the end: loaded, not used
-            sa[u] = srow[t];
+        for (int a = 0; a < MT; ++a)
+            own[a] = *reinterpret_cast<const u32x4*>(meta + (row[a] * kb + min(t0 + q, tend - 1)) * 4);
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                av[u][a] = *reinterpret_cast<const i32x4*>(values + (row[a] * kb + t) * 64 + 16 * q);
-                idx[u][a] = (int)meta[(row[a] * kb + t) * 4 + q];
-            }
+        for (int p = 0; p < 4; p += kAhead) {
+            if (p > 0 && t0 + p >= tend) break;
+            i32x4 av[kAhead][MT];
+            int sa[kAhead], sx[kAhead][NT];
+            i32x8 bv[kAhead][NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if constexpr (QX) {
-                    bv[u][j] = quant_fragment(static_cast<const uint16_t*>(X) + col[j] * ldx, 128 * (int64_t)t, k,
-                                              xvec, q, &sx[u][j]);
-                    sx[u][j] += 127;
-                } else {
-                    const uint8_t* x = static_cast<const uint8_t*>(X) + col[j] * ldx + 128 * (int64_t)t + 16 * q;
-                    bv[u][j] = join(*reinterpret_cast<const u32x4*>(x), *reinterpret_cast<const u32x4*>(x + 64));
-                    sx[u][j] = xs[t * n + col[j]];
+            for (int u = 0; u < kAhead; ++u) {
+                const int t = min(t0 + p + u, tend - 1);  // behind the end: loaded, not used
+                sa[u] = srow[t];
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+                    av[u][a] = *reinterpret_cast<const i32x4*>(values + (row[a] * kb + t) * 64 + 16 * q);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    if constexpr (QX) {
+                        bv[u][j] = quant_fragment(static_cast<const uint16_t*>(X) + col[j] * ldx, 128 * (int64_t)t,
+                                                  k, xvec, q, &sx[u][j]);
+                        sx[u][j] += 127;
+                    } else {
+                        const uint8_t* x = static_cast<const uint8_t*>(X) + col[j] * ldx + 128 * (int64_t)t + 16 * q;
+                        bv[u][j] = join(*reinterpret_cast<const u32x4*>(x), *reinterpret_cast<const u32x4*>(x + 64));
+                        sx[u][j] = xs[t * n + col[j]];
+                    }
                 }
             }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // all loads first
+            __builtin_amdgcn_sched_barrier(0);  // all loads first
+            if (p == 0)
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (t0 + u >= tend) break;
+                for (int a = 0; a < MT; ++a) words_of_blocks(own[a], idx[a]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float f = scale_product(sa[u], sx[u][j]);
+            for (int u = 0; u < kAhead; ++u) {
+                if (t0 + p + u >= tend) break;
 #pragma unroll
-                for (int a = 0; a < MT; ++a) {
-                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
-                    d = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(av[u][a], bv[u][j], d, idx[u][a], 0, 0);
+                for (int j = 0; j < NT; ++j) {
+                    const float f = scale_product(sa[u], sx[u][j]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[a][j][i] = __builtin_fmaf(d[i], f, acc[a][j][i]);
+                    for (int a = 0; a < MT; ++a) {
+                        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                        d = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(av[u][a], bv[u][j], d, (int)idx[a][p + u], 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[a][j][i] = __builtin_fmaf(d[i], f, acc[a][j][i]);
+                    }
                 }
             }
         }

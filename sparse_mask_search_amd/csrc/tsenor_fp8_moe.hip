@@ -23,7 +23,6 @@
 // they would read pieces of 32 bytes, at half the rate of the address unit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <cstdlib>
 
 #include "tsenor_fp8_device.h"
 #include "tsenor_internal.h"
@@ -118,6 +117,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 // order: the slot t * topk + rank, and t in the upper 16 bits.  The last entry is repeated
 // up to a multiple of 16.
 constexpr int kRouteWaves = 16, kMaxExperts = 512;
+template <int kHeld>  // experts of a lane: 64 kHeld in all
 __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(MoeJob a, int groups) {
     __shared__ uint16_t taken[kMaxTokens * kMaxTop];
     __shared__ unsigned long long tokens[kMaxExperts];  // bit t: token t chose the expert
@@ -128,13 +128,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(MoeJob a, i
     if (tid < kMaxExperts) tokens[tid] = 0ull;
     __syncthreads();
     for (int t = wave; t < n; t += kRouteWaves) {
-        double l[8];
-        uint64_t key[8];
+        double l[kHeld];
+        uint64_t key[kHeld];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] = lane + 64 * i < experts ? a.logits[(lane + 64 * i) * n + t] : 0.0;
+        for (int i = 0; i < kHeld; ++i) l[i] = lane + 64 * i < experts ? a.logits[(lane + 64 * i) * n + t] : 0.0;
         uint32_t left = 0u;  // this lane's experts that are not taken yet
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kHeld; ++i) {
             key[i] = logit_key(l[i]);
             left |= lane + 64 * i < experts ? 1u << i : 0u;
         }
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(MoeJob a, i
             uint64_t best = 0u;
             int at = -1;
 #pragma unroll
-            for (int i = 7; i >= 0; --i)  // downwards: of equal keys the lowest expert stays
+            for (int i = kHeld - 1; i >= 0; --i)  // downwards: of equal keys the lowest expert stays
                 if ((left >> i) & 1u && key[i] >= best) {
                     best = key[i];
                     at = i;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(MoeJob a, i
             const int e = kMaxExperts - (int)wave_max(in && (uint32_t)best == lo ? kMaxExperts - (lane + 64 * at) : 0u);
             double v = 0.0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v = (e >> 6) == i ? l[i] : v;
+            for (int i = 0; i < kHeld; ++i) v = (e >> 6) == i ? l[i] : v;
             v = __shfl(v, e & 63, 64);
             if ((e & 63) == lane) left &= ~(1u << (e >> 6));
             if (lane == r) {
@@ -248,7 +248,6 @@ __global__ __launch_bounds__(64 * kWaves) void moe_hidden_kernel(MoeJob a) {
     const int64_t f0 = (blockIdx.x - j * ft) * (16 * MT);
     const int count = a.counts[j], e = a.chosen[j], first = a.lists[j * kMaxTokens + l16];
     if (count == 0) return;
-    constexpr int kAhead = 2;
     const int kb = (int)((a.d + 127) / 128);
     const int64_t dp = kb * 128, fp = pad128(a.f);
     int64_t row[MT];
@@ -262,40 +261,54 @@ __global__ __launch_bounds__(64 * kWaves) void moe_hidden_kernel(MoeJob a) {
         f32x4 acc[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int t0 = tbegin; t0 < tend; t0 += kAhead) {
-            u32x4 v[kAhead][MT][2];
-            uint32_t idx[kAhead][MT][2];
-            int sc[kAhead][2];
-            bf16x16 b[kAhead][2];
+        for (int t0 = tbegin; t0 < tend; t0 += 4) {
+            uint32_t idx[MT][2][4];
+            u32x4 own[MT][2];
+            const int tq = min(t0 + q, tend - 1);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int t = min(t0 + u, tend - 1);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    v[u][m][0] = *reinterpret_cast<const u32x4*>(a.gate.values + (row[m] + t) * 64 + 16 * q);
-                    v[u][m][1] = *reinterpret_cast<const u32x4*>(a.up.values + (row[m] + t) * 64 + 16 * q);
-                    idx[u][m][0] = a.gate.meta[(row[m] + t) * 4 + q];
-                    idx[u][m][1] = a.up.meta[(row[m] + t) * 4 + q];
-                }
-                sc[u][0] = a.gate.scales[sb + t];
-                sc[u][1] = a.up.scales[sb + t];
-                load_block(x + 128 * t, q, b[u]);
+            for (int m = 0; m < MT; ++m) {
+                own[m][0] = *reinterpret_cast<const u32x4*>(a.gate.meta + (row[m] + tq) * 4);
+                own[m][1] = *reinterpret_cast<const u32x4*>(a.up.meta + (row[m] + tq) * 4);
             }
-            __builtin_amdgcn_sched_barrier(0);  // all loads first
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (t0 + u >= tend) break;
+            for (int p = 0; p < 4; p += 2) {
+                if (p > 0 && t0 + p >= tend) break;
+                u32x4 v[2][MT][2];
+                int sc[2][2];
+                bf16x16 b[2][2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int u = 0; u < 2; ++u) {
+                    const int t = min(t0 + p + u, tend - 1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        bf16x8 av[2];
-                        widen_block(v[u][m][i], scale_value(sc[u][i]), av);
-                        acc[m][i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[0], b[u][0], acc[m][i],
-                                                                              (int)idx[u][m][i], 0, 0);
-                        acc[m][i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[1], b[u][1], acc[m][i],
-                                                                              (int)(idx[u][m][i] >> 16), 0, 0);
+                    for (int m = 0; m < MT; ++m) {
+                        v[u][m][0] = *reinterpret_cast<const u32x4*>(a.gate.values + (row[m] + t) * 64 + 16 * q);
+                        v[u][m][1] = *reinterpret_cast<const u32x4*>(a.up.values + (row[m] + t) * 64 + 16 * q);
                     }
+                    sc[u][0] = a.gate.scales[sb + t];
+                    sc[u][1] = a.up.scales[sb + t];
+                    load_block(x + 128 * t, q, b[u]);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // all loads first
+                if (p == 0)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) words_of_blocks(own[m][i], idx[m][i]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (t0 + p + u >= tend) break;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            bf16x8 av[2];
+                            widen_block(v[u][m][i], scale_value(sc[u][i]), av);
+                            const uint32_t x = idx[m][i][p + u];
+                            acc[m][i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[0], b[u][0], acc[m][i], (int)x, 0, 0);
+                            acc[m][i] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[1], b[u][1], acc[m][i],
+                                                                                  (int)(x >> 16), 0, 0);
+                        }
+                }
             }
         }
 #pragma unroll
@@ -346,7 +359,6 @@ __global__ __launch_bounds__(64 * kWaves) void moe_down_kernel(MoeJob a) {
     const int64_t d0 = (blockIdx.x - j * dt) * (16 * MT);
     const int count = a.counts[j], e = a.chosen[j], first = a.lists[j * kMaxTokens + l16];
     if (count == 0) return;
-    constexpr int kAhead = 2;
     const int kb = (int)((a.f + 127) / 128);
     const int64_t fp = kb * 128, lo_at = a.n * a.topk * fp, dp = (a.d + 3) & ~(int64_t)3;
     int64_t row[MT];
@@ -360,36 +372,45 @@ __global__ __launch_bounds__(64 * kWaves) void moe_down_kernel(MoeJob a) {
         f32x4 acc[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int t0 = tbegin; t0 < tend; t0 += kAhead) {
-            u32x4 v[kAhead][MT];
-            uint32_t idx[kAhead][MT];
-            int sc[kAhead];
-            bf16x16 hi[kAhead][2], lo[kAhead][2];
+        for (int t0 = tbegin; t0 < tend; t0 += 4) {
+            uint32_t idx[MT][4];
+            u32x4 own[MT];
+            const int tq = min(t0 + q, tend - 1);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int t = min(t0 + u, tend - 1);
+            for (int m = 0; m < MT; ++m) own[m] = *reinterpret_cast<const u32x4*>(a.down.meta + (row[m] + tq) * 4);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    v[u][m] = *reinterpret_cast<const u32x4*>(a.down.values + (row[m] + t) * 64 + 16 * q);
-                    idx[u][m] = a.down.meta[(row[m] + t) * 4 + q];
+            for (int p = 0; p < 4; p += 2) {
+                if (p > 0 && t0 + p >= tend) break;
+                u32x4 v[2][MT];
+                int sc[2];
+                bf16x16 hi[2][2], lo[2][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = min(t0 + p + u, tend - 1);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        v[u][m] = *reinterpret_cast<const u32x4*>(a.down.values + (row[m] + t) * 64 + 16 * q);
+                    sc[u] = a.down.scales[sb + t];
+                    load_block(h + 128 * t, q, hi[u]);
+                    load_block(h + lo_at + 128 * t, q, lo[u]);
                 }
-                sc[u] = a.down.scales[sb + t];
-                load_block(h + 128 * t, q, hi[u]);
-                load_block(h + lo_at + 128 * t, q, lo[u]);
-            }
-            __builtin_amdgcn_sched_barrier(0);  // all loads first
+                __builtin_amdgcn_sched_barrier(0);  // all loads first
+                if (p == 0)
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (t0 + u >= tend) break;
+                    for (int m = 0; m < MT; ++m) words_of_blocks(own[m], idx[m]);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    bf16x8 av[2];
-                    widen_block(v[u][m], scale_value(sc[u]), av);
+                for (int u = 0; u < 2; ++u) {
+                    if (t0 + p + u >= tend) break;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int x = (int)(idx[u][m] >> (16 * i));
-                        acc[m] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], hi[u][i], acc[m], x, 0, 0);
-                        acc[m] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], lo[u][i], acc[m], x, 0, 0);
+                    for (int m = 0; m < MT; ++m) {
+                        bf16x8 av[2];
+                        widen_block(v[u][m], scale_value(sc[u]), av);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int x = (int)(idx[m][p + u] >> (16 * i));
+                            acc[m] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], hi[u][i], acc[m], x, 0, 0);
+                            acc[m] = __builtin_amdgcn_smfmac_f32_16x16x64_bf16(av[i], lo[u][i], acc[m], x, 0, 0);
+                        }
                     }
                 }
             }
@@ -437,22 +458,26 @@ int launch_moe24_fp8(const MoeJob& a, void* stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
     const int64_t groups = a.n * a.topk < a.experts ? a.n * a.topk : a.experts;  // chosen experts at most
-    hipLaunchKernelGGL(moe_route_kernel, dim3(1), dim3(64 * kRouteWaves), 0, s, a, (int)groups);
+    const auto route = a.experts <= 64 ? moe_route_kernel<1> : a.experts <= 128 ? moe_route_kernel<2> : moe_route_kernel<8>;
+    hipLaunchKernelGGL(route, dim3(1), dim3(64 * kRouteWaves), 0, s, a, (int)groups);
     e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    const auto tiles = [&](int rows) { return groups * ((a.f + rows - 1) / rows); };
+    // Rows of a workgroup: 64, so that a token's activations are read once for four tiles, or
+    // 16 where that would leave too few workgroups.  Measured (us) with 64 / 16 rows: hidden, one
+    // token, 6 experts, 2048 x 1408: 13.3 / 11.4; 33 tokens, 16 experts, 4096 x 2048: 38 / 43;
+    // down: 5.5 / 7.6 and 30 / 54.
+    const auto tiles = [&](int64_t length, int rows) { return groups * ((length + rows - 1) / rows); };
     const dim3 threads(64 * kWaves);
-    const int v = getenv("MTV") ? atoi(getenv("MTV")) : 0;
-    if (v == 4 || (v == 0 && tiles(32) > 512)) hipLaunchKernelGGL(moe_hidden_kernel<4>, dim3((unsigned)tiles(64)), threads, 0, s, a);
-    else if (v == 2 || (v == 0 && tiles(16) > 512)) hipLaunchKernelGGL(moe_hidden_kernel<2>, dim3((unsigned)tiles(32)), threads, 0, s, a);
-    else hipLaunchKernelGGL(moe_hidden_kernel<1>, dim3((unsigned)tiles(16)), threads, 0, s, a);
+    if (tiles(a.f, 64) >= 256)
+        hipLaunchKernelGGL(moe_hidden_kernel<4>, dim3((unsigned)tiles(a.f, 64)), threads, 0, s, a);
+    else
+        hipLaunchKernelGGL(moe_hidden_kernel<1>, dim3((unsigned)tiles(a.f, 16)), threads, 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    const auto dtiles = [&](int rows) { return groups * ((a.d + rows - 1) / rows); };
-    const int w = getenv("MDV") ? atoi(getenv("MDV")) : 0;
-    if (w == 4 || (w == 0 && dtiles(32) > 1024)) hipLaunchKernelGGL(moe_down_kernel<4>, dim3((unsigned)dtiles(64)), threads, 0, s, a);
-    else if (w == 2 || (w == 0 && dtiles(16) > 1024)) hipLaunchKernelGGL(moe_down_kernel<2>, dim3((unsigned)dtiles(32)), threads, 0, s, a);
-    else hipLaunchKernelGGL(moe_down_kernel<1>, dim3((unsigned)dtiles(16)), threads, 0, s, a);
+    if (tiles(a.d, 64) >= 128)
+        hipLaunchKernelGGL(moe_down_kernel<4>, dim3((unsigned)tiles(a.d, 64)), threads, 0, s, a);
+    else
+        hipLaunchKernelGGL(moe_down_kernel<1>, dim3((unsigned)tiles(a.d, 16)), threads, 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
     hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)(a.n * ((a.d + 1023) / 1024))), dim3(256), 0, s, a);
