@@ -39,7 +39,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ X
 }
 
 // Along the columns, and along the rows too when `values` is given: one
-// workgroup per 128 x 128 tile, read once and kept in LDS.
+// workgroup per 128 x 128 tile, read once and kept in LDS.  A thread holds a part of one
+// column (f32: 64 rows) or of two (bf16: 32 rows of a pair, one LDS word a row) in registers;
+// the 8-bit columns leave through LDS, so that eight lanes write the 128 bytes of a column
+// side by side (written by the threads that hold them, each store would touch 64 lines).
 template <class T>
 __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X, int64_t rows,
                                                          int64_t cols, int64_t ldx, bool vec,
@@ -47,12 +50,17 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X
                                                          uint8_t* __restrict__ scales,
                                                          uint8_t* __restrict__ values_t,
                                                          uint8_t* __restrict__ scales_t) {
-    constexpr int kLd = 128 + 16 / sizeof(T);
-    __shared__ T tile[128 * kLd];
-    __shared__ uint32_t colmax[2][128];
+    constexpr bool kPairs = sizeof(T) == 2;
+    constexpr int kLd = 128 + 16 / sizeof(T), kOut = 144;  // a tile row's elements, an output column's bytes
+    constexpr int kParts = kPairs ? 4 : 2, kLen = 128 / kParts;
+    __shared__ __attribute__((aligned(16))) T tile[128 * kLd];
+    __shared__ uint32_t colmax[kParts][128];
+    uint8_t* out = reinterpret_cast<uint8_t*>(tile);  // after the tile has been read
+    static_assert(128 * kOut <= (int)sizeof(tile), "output columns fit the tile's place");
     const int64_t cblocks = (cols + 127) / 128, rblocks = (rows + 127) / 128;
     const int64_t rb = blockIdx.x / cblocks, cb = blockIdx.x - rb * cblocks;
     const int tid = threadIdx.x, l = tid & 15;
+#pragma unroll 4
     for (int p = 0; p < 8; ++p) {
         const int lr = 16 * p + (tid >> 4);
         const int64_t r = rb * 128 + lr;
@@ -82,56 +90,78 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X
         }
     }
     __syncthreads();
-    // a thread holds half a column (64 rows)
-    const int c = tid & 127, half = tid >> 7;
-    uint32_t m = 0u;
-    for (int i = 0; i < 64; ++i) m = max(m, finite_magnitude(widen(tile[(64 * half + i) * kLd + c])));
-    colmax[half][c] = m;
-    __syncthreads();
-    const int64_t col = cb * 128 + c;
-    if (col >= cols) return;
-    const int s = scale_exponent(max(colmax[0][c], colmax[1][c]));
-    const float inv = inverse_scale(s);
-    uint8_t* out = values_t + col * (rblocks * 128) + rb * 128 + 64 * half;
-    for (int v = 0; v < 4; ++v) {
-        u32x4 q;
+    const int c = kPairs ? 2 * (tid & 63) : tid & 127, part = kPairs ? tid >> 6 : tid >> 7;
+    uint32_t w[kLen], m0 = 0u, m1 = 0u;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[i] = scaled(widen(tile[(64 * half + 16 * v + 4 * w + i) * kLd + c]), inv);
-            q[w] = pack4(y[0], y[1], y[2], y[3]);
+    for (int i = 0; i < kLen; ++i) {
+        w[i] = *reinterpret_cast<const uint32_t*>(&tile[(kLen * part + i) * kLd + c]);
+        if constexpr (kPairs) {
+            m0 = max(m0, finite_magnitude(bits_float(w[i] << 16)));
+            m1 = max(m1, finite_magnitude(bits_float(w[i] & 0xFFFF0000u)));
+        } else {
+            m0 = max(m0, finite_magnitude(bits_float(w[i])));
         }
-        *reinterpret_cast<u32x4*>(out + 16 * v) = q;
     }
-    if (half == 0) scales_t[rb * cols + col] = (uint8_t)(s + 127);
+    colmax[part][c] = m0;
+    if constexpr (kPairs) colmax[part][c + 1] = m1;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < (kPairs ? 2 : 1); ++k) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) m = max(m, colmax[i][c + k]);
+        const int s = scale_exponent(m);
+        const float inv = inverse_scale(s);
+        const auto entry = [&](int i) {
+            return scaled(bits_float(!kPairs ? w[i] : k ? w[i] & 0xFFFF0000u : w[i] << 16), inv);
+        };
+#pragma unroll
+        for (int v = 0; v < kLen; v += 16) {
+            u32x4 q;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[e] = pack4(entry(v + 4 * e), entry(v + 4 * e + 1), entry(v + 4 * e + 2), entry(v + 4 * e + 3));
+            *reinterpret_cast<u32x4*>(out + (c + k) * kOut + kLen * part + v) = q;
+        }
+        if (part == 0 && cb * 128 + c + k < cols) scales_t[rb * cols + cb * 128 + c + k] = (uint8_t)(s + 127);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int u = tid + 256 * i, col = u >> 3, chunk = 16 * (u & 7);
+        if (cb * 128 + col < cols)
+            *reinterpret_cast<u32x4*>(values_t + (cb * 128 + col) * (rblocks * 128) + rb * 128 + chunk) =
+                *reinterpret_cast<const u32x4*>(out + col * kOut + chunk);
+    }
 }
 
 // First two set bits of a group's four mask bits, as the four bits of its
-// metadata (unused slots point at a free position), and its two values.
-__device__ __forceinline__ uint32_t take24(uint32_t bits, uint32_t q, uint32_t* v0, uint32_t* v1,
-                                           int* over) {
+// metadata (unused slots point at a free position), and its two values (16 bits).
+__device__ __forceinline__ uint32_t take24(uint32_t bits, uint32_t q, uint32_t* v, int* over) {
     const uint32_t rest = bits & (bits - 1u);
-    uint32_t p0 = bits ? (uint32_t)__builtin_ctz(bits) : 0u;
-    uint32_t p1 = rest ? (uint32_t)__builtin_ctz(rest) : (bits ? (p0 == 3u ? 2u : 3u) : 1u);
-    *v0 = bits ? (q >> (8 * p0)) & 0xFFu : 0u;
-    *v1 = rest ? (q >> (8 * p1)) & 0xFFu : 0u;
+    const uint32_t p0 = bits ? (uint32_t)__builtin_ctz(bits) : 0u;
+    const uint32_t p1 = rest ? (uint32_t)__builtin_ctz(rest) : (bits ? (p0 == 3u ? 2u : 3u) : 1u);
+    const uint32_t v0 = bits ? (q >> (8 * p0)) & 0xFFu : 0u, v1 = rest ? (q >> (8 * p1)) & 0xFFu : 0u;
+    *v = v0 | (v1 << 8);
     *over += (rest & (rest - 1u)) != 0u;
     return p0 | (p1 << 2);
 }
 
 // One workgroup per 128 x 128 tile of one matrix.  The tile's kept entries
-// give the one scale that both orientations share; the 8-bit numbers go to LDS
-// once, and are compressed from there along the rows and along the columns.
+// give the one scale that both orientations share.  The rows are compressed from the
+// registers that hold them (16 lanes a row, two groups each); for the columns the 8-bit
+// numbers go to LDS, a thread turns 4 x 4 cells of them around with byte permutations, and
+// the compressed columns leave through LDS as whole lines.
 template <class T>
 __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     const T* __restrict__ W, int64_t stride, int64_t rows, int64_t cols, int64_t ld, bool vec,
     const uint32_t* __restrict__ mask, uint8_t* __restrict__ values, uint32_t* __restrict__ meta,
     uint8_t* __restrict__ scales, uint8_t* __restrict__ values_t, uint32_t* __restrict__ meta_t,
     uint8_t* __restrict__ scales_t, int* __restrict__ bad, int* __restrict__ bad_t) {
-    constexpr int kLd = 144;  // bytes of a tile row
+    constexpr int kLd = 132, kOut = 80;  // bytes of a tile row, of a compressed column
     __shared__ __attribute__((aligned(16))) uint8_t q8[128 * kLd];
+    __shared__ __attribute__((aligned(16))) uint8_t out[128 * kOut];
+    __shared__ __attribute__((aligned(16))) uint16_t out_meta[128 * 8];
     __shared__ uint32_t bits[128][5];  // mask words of the tile's rows (padded against bank conflicts)
     __shared__ uint32_t wmax[4];
     const int64_t cblocks = (cols + 127) / 128, rblocks = (rows + 127) / 128;
@@ -142,6 +172,17 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     const int tid = threadIdx.x, l = tid & 15;
     W += mat * stride;
     mask += mat * rows * wpr;
+    T raw[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int64_t r = rb * 128 + 16 * p + (tid >> 4);
+        if (r < rows) {
+            load8(W + r * ld, cb * 128 + 8 * l, cols, vec, raw[p]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[p][i] = (T)0;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int lr = (tid + 256 * i) >> 2, w = tid & 3;
@@ -155,19 +196,10 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
         bits[lr][w] = m;
     }
     __syncthreads();
-    T raw[8][8];
     uint32_t m = 0u;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const int lr = 16 * p + (tid >> 4);
-        const int64_t r = rb * 128 + lr;
-        if (r < rows) {
-            load8(W + r * ld, cb * 128 + 8 * l, cols, vec, raw[p]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) raw[p][i] = (T)0;
-        }
-        const uint32_t keep = bits[lr][l >> 2] >> (8 * (l & 3));
+        const uint32_t keep = bits[16 * p + (tid >> 4)][l >> 2] >> (8 * (l & 3));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (!((keep >> i) & 1u)) raw[p][i] = (T)0;
@@ -181,68 +213,82 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     __syncthreads();
     const int s = scale_exponent(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
     const float inv = inverse_scale(s);
+    int over = 0;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int lr = 16 * p + (tid >> 4);
+        const int64_t r = rb * 128 + lr;
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = scaled(widen(raw[p][i]), inv);
-        const u32x2 q = {pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7])};
-        *reinterpret_cast<u32x2*>(&q8[lr * kLd + 8 * l]) = q;
+        const uint32_t q0 = pack4(y[0], y[1], y[2], y[3]), q1 = pack4(y[4], y[5], y[6], y[7]);
+        if (values != nullptr) {  // uniform
+            const uint32_t keep = bits[lr][l >> 2] >> (8 * (l & 3));
+            uint32_t v0, v1;
+            const uint32_t n0 = take24(keep & 15u, q0, &v0, &over), n1 = take24((keep >> 4) & 15u, q1, &v1, &over);
+            uint32_t word = (n0 | (n1 << 4)) << (8 * (l & 3));  // four lanes share a word
+            word |= (uint32_t)__shfl_xor(word, 1, 64);
+            word |= (uint32_t)__shfl_xor(word, 2, 64);
+            if (r < rows) {
+                const int64_t at = (mat * rows + r) * cblocks + cb;
+                *reinterpret_cast<uint32_t*>(values + at * 64 + 4 * l) = v0 | (v1 << 16);
+                if ((l & 3) == 0) meta[at * 4 + (l >> 2)] = word;
+            }
+        }
+        if (values_t != nullptr) {
+            *reinterpret_cast<uint32_t*>(&q8[lr * kLd + 8 * l]) = q0;
+            *reinterpret_cast<uint32_t*>(&q8[lr * kLd + 8 * l + 4]) = q1;
+        }
     }
+    if (over && bad != nullptr) atomicAdd(bad, over);
     if (tid == 0) {
         if (scales != nullptr) scales[mat * per + rb * cblocks + cb] = (uint8_t)(s + 127);
         if (scales_t != nullptr) scales_t[mat * per + cb * rblocks + rb] = (uint8_t)(s + 127);
     }
+    if (values_t == nullptr) return;
     __syncthreads();
-    const int a = tid & 127, half = tid >> 7;  // a row (or column) and 64 entries along it
-    if (values != nullptr && rb * 128 + a < rows) {
-        const int64_t r = mat * rows + rb * 128 + a;
-        int over = 0;
-        uint32_t out[8], mw[2] = {0u, 0u};
+    over = 0;
+    const int cq = tid & 31, part = tid >> 5;  // four columns, 16 rows
+    uint32_t v[4][2] = {}, mw[4] = {};
 #pragma unroll
-        for (int g = 0; g < 16; g += 2) {
-            const int c = 64 * half + 4 * g;
-            const uint32_t word = bits[a][c >> 5];
-            uint32_t v[4];
-            const uint32_t n0 = take24((word >> (c & 31)) & 15u,
-                                       *reinterpret_cast<const uint32_t*>(&q8[a * kLd + c]), v, v + 1, &over);
-            const uint32_t n1 = take24((word >> ((c & 31) + 4)) & 15u,
-                                       *reinterpret_cast<const uint32_t*>(&q8[a * kLd + c + 4]), v + 2,
-                                       v + 3, &over);
-            out[g / 2] = v[0] | (v[1] << 8) | (v[2] << 16) | (v[3] << 24);
-            mw[g >> 3] |= (n0 << (4 * (g & 7))) | (n1 << (4 * ((g + 1) & 7)));
+    for (int g = 0; g < 4; ++g) {
+        uint32_t q[4], kept = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * part + 4 * g + i;
+            q[i] = *reinterpret_cast<const uint32_t*>(&q8[r * kLd + 4 * cq]);
+            kept |= ((bits[r][cq >> 3] >> (4 * (cq & 7))) & 15u) << (4 * i);
         }
-        u32x4* ov = reinterpret_cast<u32x4*>(values + r * (cblocks * 64) + cb * 64 + 32 * half);
-        ov[0] = u32x4{out[0], out[1], out[2], out[3]};
-        ov[1] = u32x4{out[4], out[5], out[6], out[7]};
-        *reinterpret_cast<u32x2*>(meta + r * (cblocks * 4) + cb * 4 + 2 * half) = u32x2{mw[0], mw[1]};
-        if (over && bad != nullptr) atomicAdd(bad, over);
-    }
-    if (values_t != nullptr && cb * 128 + a < cols) {
-        const int64_t c = mat * cols + cb * 128 + a;
-        int over = 0;
-        uint32_t out[8], mw[2] = {0u, 0u};
+        // bytes of four rows to bytes of four columns
+        const uint32_t a = __builtin_amdgcn_perm(q[1], q[0], 0x05010400u), b = __builtin_amdgcn_perm(q[3], q[2], 0x05010400u);
+        const uint32_t c = __builtin_amdgcn_perm(q[1], q[0], 0x07030602u), d = __builtin_amdgcn_perm(q[3], q[2], 0x07030602u);
+        const uint32_t col[4] = {__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(b, a, 0x07060302u),
+                                 __builtin_amdgcn_perm(d, c, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
 #pragma unroll
-        for (int g = 0; g < 16; g += 2) {
-            uint32_t b[2] = {0u, 0u}, q[2] = {0u, 0u}, v[4], n[2];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 64 * half + 4 * g + i;
-                b[i >> 2] |= ((bits[r][a >> 5] >> (a & 31)) & 1u) << (i & 3);
-                q[i >> 2] |= (uint32_t)q8[r * kLd + a] << (8 * (i & 3));
-            }
-            n[0] = take24(b[0], q[0], v, v + 1, &over);
-            n[1] = take24(b[1], q[1], v + 2, v + 3, &over);
-            out[g / 2] = v[0] | (v[1] << 8) | (v[2] << 16) | (v[3] << 24);
-            mw[g >> 3] |= (n[0] << (4 * (g & 7))) | (n[1] << (4 * ((g + 1) & 7)));
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t x = (kept >> j) & 0x1111u;  // this column's bits, one in each nibble
+            uint32_t two;
+            mw[j] |= take24((x | (x >> 3) | (x >> 6) | (x >> 9)) & 15u, col[j], &two, &over) << (4 * g);
+            v[j][g >> 1] |= two << (16 * (g & 1));
         }
-        u32x4* ov = reinterpret_cast<u32x4*>(values_t + c * (rblocks * 64) + rb * 64 + 32 * half);
-        ov[0] = u32x4{out[0], out[1], out[2], out[3]};
-        ov[1] = u32x4{out[4], out[5], out[6], out[7]};
-        *reinterpret_cast<u32x2*>(meta_t + c * (rblocks * 4) + rb * 4 + 2 * half) = u32x2{mw[0], mw[1]};
-        if (over && bad_t != nullptr) atomicAdd(bad_t, over);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        *reinterpret_cast<u32x2*>(&out[(4 * cq + j) * kOut + 8 * part]) = u32x2{v[j][0], v[j][1]};
+        out_meta[(4 * cq + j) * 8 + part] = (uint16_t)mw[j];
+    }
+    if (over && bad_t != nullptr) atomicAdd(bad_t, over);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int u = tid + 256 * i, c = u >> 2, chunk = 16 * (u & 3);
+        if (cb * 128 + c < cols)
+            *reinterpret_cast<u32x4*>(values_t + ((mat * cols + cb * 128 + c) * rblocks + rb) * 64 + chunk) =
+                *reinterpret_cast<const u32x4*>(&out[c * kOut + chunk]);
+    }
+    if (tid < 128 && cb * 128 + tid < cols)
+        *reinterpret_cast<u32x4*>(meta_t + ((mat * cols + cb * 128 + tid) * rblocks + rb) * 4) =
+            *reinterpret_cast<const u32x4*>(&out_meta[tid * 8]);
 }
 
 template <class T>
