@@ -22,13 +22,6 @@ __device__ __forceinline__ uint32_t float_bits(float x) { return __builtin_bit_c
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 
 __device__ __forceinline__ float widen(uint16_t b) { return bits_float((uint32_t)b << 16); }
-__device__ __forceinline__ float widen(float x) { return x; }
-
-// |x| as an integer that orders like the magnitude; 0 for infinities and NaN.
-__device__ __forceinline__ uint32_t finite_magnitude(float x) {
-    const uint32_t a = float_bits(x) & 0x7FFFFFFFu;
-    return a < 0x7F800000u ? a : 0u;
-}
 
 // The scale exponent s of a block: least s >= -127 with amax <= 448 * 2^s.
 // With amax = 1.f * 2^(E-127) and 448 = 1.75 * 2^8, s = E-135 if 1.f <= 1.75
@@ -49,11 +42,6 @@ __device__ __forceinline__ float scale_product(int a, int b) {
     const uint32_t normal = (uint32_t)min(e, 254) << 23;
     const uint32_t subnormal = 0x400000u >> min(max(-e, 0), 31);
     return bits_float(e >= 1 ? normal : subnormal);
-}
-
-// x * 2^-s before the conversion; infinities become NaN like NaN itself.
-__device__ __forceinline__ float scaled(float x, float inv) {
-    return (float_bits(x) & 0x7F800000u) == 0x7F800000u ? bits_float(0x7FC00000u) : x * inv;
 }
 
 // Four e4m3 numbers, nearest even.  |arguments| <= 448 or NaN.
@@ -101,6 +89,113 @@ __device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols,
         for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.f;
     }
 }
+
+// Eight neighbouring entries in registers, bf16 as four pairs.  Magnitudes order like the
+// bits below the sign, so a maximum needs no conversion; one of kSpecial or more tells of an
+// infinity or a NaN, and only then are entries looked at one by one (finite_only).
+constexpr uint32_t kSpecial = 0x7F800000u;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 pair_max(u16x2 m, uint32_t w) {
+    return __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu));
+}
+// The magnitude of a pair's larger entry, as fp32 bits.
+__device__ __forceinline__ uint32_t pair_magnitude(u16x2 m) {
+    return (uint32_t)max(m[0], m[1]) << 16;
+}
+// Infinities of a pair become NaN; the larger finite magnitude.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t* w) {
+    const uint32_t lo = *w & 0x7FFFu, hi = (*w >> 16) & 0x7FFFu;
+    if (lo >= 0x7F80u) *w |= 0x7FFFu;
+    if (hi >= 0x7F80u) *w |= 0x7FFF0000u;
+    return max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u) << 16;
+}
+__device__ __forceinline__ uint32_t finite_one(uint32_t* w) {
+    const uint32_t a = *w & 0x7FFFFFFFu;
+    if (a >= kSpecial) *w |= 0x7FFFFFFFu;
+    return a < kSpecial ? a : 0u;
+}
+// Entries of two pairs (of four fp32 words) as e4m3.
+__device__ __forceinline__ uint32_t pack_pairs(uint32_t a, uint32_t b, float inv) {
+    return pack4(bits_float(a << 16) * inv, bits_float(a & 0xFFFF0000u) * inv, bits_float(b << 16) * inv,
+                 bits_float(b & 0xFFFF0000u) * inv);
+}
+__device__ __forceinline__ uint32_t pack_words(uint32_t a, uint32_t b, uint32_t c, uint32_t d, float inv) {
+    return pack4(bits_float(a) * inv, bits_float(b) * inv, bits_float(c) * inv, bits_float(d) * inv);
+}
+
+template <class T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const uint16_t* row, int64_t c, int64_t cols, bool vec) {
+        uint16_t v[8];
+        load8(row, c, cols, vec, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)v[2 * i] | ((uint32_t)v[2 * i + 1] << 16);
+    }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void keep(uint32_t bits) {  // bit i: entry i stays
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe((int)bits, 2 * i, 1);
+            const uint32_t hi = (uint32_t)__builtin_amdgcn_sbfe((int)bits, 2 * i + 1, 1);
+            w[i] &= (lo & 0xFFFFu) | (hi & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ uint32_t magnitude() const {
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = pair_max(m, w[i]);
+        return pair_magnitude(m);
+    }
+    __device__ __forceinline__ uint32_t finite_only() {
+        return max(max(finite_pair(w), finite_pair(w + 1)), max(finite_pair(w + 2), finite_pair(w + 3)));
+    }
+    __device__ __forceinline__ u32x2 quantised(float inv) const {
+        return u32x2{pack_pairs(w[0], w[1], inv), pack_pairs(w[2], w[3], inv)};
+    }
+    __device__ __forceinline__ void store(uint16_t* to) const {
+        *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+    }
+};
+template <>
+struct Eight<float> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const float* row, int64_t c, int64_t cols, bool vec) {
+        float v[8];
+        load8(row, c, cols, vec, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = float_bits(v[i]);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void keep(uint32_t bits) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] &= (uint32_t)__builtin_amdgcn_sbfe((int)bits, i, 1);
+    }
+    __device__ __forceinline__ uint32_t magnitude() const {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+        return m;
+    }
+    __device__ __forceinline__ uint32_t finite_only() {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, finite_one(w + i));
+        return m;
+    }
+    __device__ __forceinline__ u32x2 quantised(float inv) const {
+        return u32x2{pack_words(w[0], w[1], w[2], w[3], inv), pack_words(w[4], w[5], w[6], w[7], inv)};
+    }
+    __device__ __forceinline__ void store(float* to) const {
+        *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+        *reinterpret_cast<u32x4*>(to + 4) = u32x4{w[4], w[5], w[6], w[7]};
+    }
+};
 
 // Direct loads from global memory to LDS, from a uniform base plus the lane's
 // offset: lane l's 16 bytes (or 4, or its byte widened to 32 bits) land at the LDS

@@ -45,60 +45,28 @@ __device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
     return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
-// Two bf16 entries (a 32-bit word) times inv, as fp32.
-__device__ __forceinline__ void scale2(uint32_t w, float inv, float* lo, float* hi) {
-    *lo = bits_float(w << 16) * inv;
-    *hi = bits_float(w & 0xFFFF0000u) * inv;
-}
-
 // This lane's part of one block of a bf16 row (entries 16q .. and 64+16q .. of
 // the 128 at k0), quantised; the four lanes that hold the block share its scale.
-// Magnitudes of bf16 numbers order like their low 15 bits, so the maximum runs on
-// pairs (16 and-s and 16 packed maxima); only a block with an infinity or a NaN
-// (a maximum of 0x7F80 or more) looks at its entries one by one.
 __device__ __forceinline__ i32x8 quant_fragment(const uint16_t* row, int64_t k0, int64_t k, bool vec,
                                                 int q, int* s) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    uint32_t w[16];
+    Eight<uint16_t> v[4];
+    uint32_t m = 0u;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        uint16_t v[8];
-        load8(row, k0 + 16 * q + 64 * (p >> 1) + 8 * (p & 1), k, vec, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * p + i] = (uint32_t)v[2 * i] | ((uint32_t)v[2 * i + 1] << 16);
+        v[p].load(row, k0 + 16 * q + 64 * (p >> 1) + 8 * (p & 1), k, vec);
+        m = max(m, v[p].magnitude());
     }
-    u16x2 m2 = {0, 0};
+    if (__any(m >= kSpecial)) {
+        m = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        m2 = __builtin_elementwise_max(m2, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
-    uint32_t m = max((uint32_t)m2[0], (uint32_t)m2[1]);
-    const bool special = m >= 0x7F80u;
-    if (__any(special)) {
-        if (special) {
-            m = 0u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                // infinities become NaN, which the conversion keeps; zeros count as magnitudes
-                const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-                m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-                if (lo >= 0x7F80u) w[i] |= 0x7FFFu;
-                if (hi >= 0x7F80u) w[i] |= 0x7FFF0000u;
-            }
-        }
+        for (int p = 0; p < 4; ++p) m = max(m, v[p].finite_only());
     }
     m = max(m, (uint32_t)__shfl_xor(m, 16, 64));
     m = max(m, (uint32_t)__shfl_xor(m, 32, 64));
-    *s = scale_exponent(m << 16);
+    *s = scale_exponent(m);
     const float inv = inverse_scale(*s);
-    i32x8 r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float a, b, c, d;
-        scale2(w[2 * i], inv, &a, &b);
-        scale2(w[2 * i + 1], inv, &c, &d);
-        r[i] = (int)pack4(a, b, c, d);
-    }
-    return r;
+    const u32x2 a = v[0].quantised(inv), b = v[1].quantised(inv), c = v[2].quantised(inv), d = v[3].quantised(inv);
+    return i32x8{(int)a.x, (int)a.y, (int)b.x, (int)b.y, (int)c.x, (int)c.y, (int)d.x, (int)d.y};
 }
 
 // Few tokens (n <= 16 NT): reading A bounds the product, so a workgroup owns 16 MT

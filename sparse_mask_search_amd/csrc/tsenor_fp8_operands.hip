@@ -23,17 +23,12 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ X
     if (g >= rows * blocks) return;
     const int64_t r = g / blocks, b = g - r * blocks;
     const int l = threadIdx.x & 15;
-    T raw[8];
-    load8(X + r * ldx, b * 128 + 8 * l, cols, vec, raw);
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(widen(raw[i])));
+    Eight<T> v;
+    v.load(X + r * ldx, b * 128 + 8 * l, cols, vec);
+    uint32_t m = v.magnitude();
+    if (__any(m >= kSpecial)) m = v.finite_only();
     const int s = scale_exponent(max16(m));
-    const float inv = inverse_scale(s);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = scaled(widen(raw[i]), inv);
-    const u32x2 q = {pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7])};
+    const u32x2 q = v.quantised(inverse_scale(s));
     *reinterpret_cast<u32x2*>(values + r * (blocks * 128) + b * 128 + 8 * l) = q;
     if (l == 0) scales[b * rows + r] = (uint8_t)(s + 127);
 }
@@ -64,27 +59,17 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X
     for (int p = 0; p < 8; ++p) {
         const int lr = 16 * p + (tid >> 4);
         const int64_t r = rb * 128 + lr;
-        T raw[8];
-        if (r < rows) {
-            load8(X + r * ldx, cb * 128 + 8 * l, cols, vec, raw);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) raw[i] = (T)0;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) tile[lr * kLd + 8 * l + i] = raw[i];
+        Eight<T> v;
+        if (r < rows) v.load(X + r * ldx, cb * 128 + 8 * l, cols, vec);
+        else v.clear();
+        v.store(&tile[lr * kLd + 8 * l]);
         if (values != nullptr) {  // uniform
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(widen(raw[i])));
+            uint32_t m = v.magnitude();
+            if (__any(m >= kSpecial)) m = v.finite_only();
             const int s = scale_exponent(max16(m));
-            const float inv = inverse_scale(s);
             if (r < rows) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = scaled(widen(raw[i]), inv);
-                const u32x2 q = {pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7])};
-                *reinterpret_cast<u32x2*>(values + r * (cblocks * 128) + cb * 128 + 8 * l) = q;
+                *reinterpret_cast<u32x2*>(values + r * (cblocks * 128) + cb * 128 + 8 * l) =
+                    v.quantised(inverse_scale(s));
                 if (l == 0) scales[cb * rows + r] = (uint8_t)(s + 127);
             }
         }
@@ -92,14 +77,29 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X
     __syncthreads();
     const int c = kPairs ? 2 * (tid & 63) : tid & 127, part = kPairs ? tid >> 6 : tid >> 7;
     uint32_t w[kLen], m0 = 0u, m1 = 0u;
+    u16x2 pairs = {0, 0};
 #pragma unroll
     for (int i = 0; i < kLen; ++i) {
         w[i] = *reinterpret_cast<const uint32_t*>(&tile[(kLen * part + i) * kLd + c]);
-        if constexpr (kPairs) {
-            m0 = max(m0, finite_magnitude(bits_float(w[i] << 16)));
-            m1 = max(m1, finite_magnitude(bits_float(w[i] & 0xFFFF0000u)));
-        } else {
-            m0 = max(m0, finite_magnitude(bits_float(w[i])));
+        if constexpr (kPairs) pairs = pair_max(pairs, w[i]);
+        else m0 = max(m0, w[i] & 0x7FFFFFFFu);
+    }
+    if constexpr (kPairs) {
+        m0 = (uint32_t)pairs[0] << 16;
+        m1 = (uint32_t)pairs[1] << 16;
+    }
+    if (__any(max(m0, m1) >= kSpecial)) {
+        m0 = m1 = 0u;
+#pragma unroll
+        for (int i = 0; i < kLen; ++i) {
+            if constexpr (kPairs) {
+                (void)finite_pair(&w[i]);  // NaN where it was not finite
+                const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+                m0 = max(m0, lo < 0x7F80u ? lo << 16 : 0u);
+                m1 = max(m1, hi < 0x7F80u ? hi << 16 : 0u);
+            } else {
+                m0 = max(m0, finite_one(&w[i]));
+            }
         }
     }
     colmax[part][c] = m0;
@@ -112,15 +112,13 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X
         for (int i = 0; i < kParts; ++i) m = max(m, colmax[i][c + k]);
         const int s = scale_exponent(m);
         const float inv = inverse_scale(s);
-        const auto entry = [&](int i) {
-            return scaled(bits_float(!kPairs ? w[i] : k ? w[i] & 0xFFFF0000u : w[i] << 16), inv);
-        };
+        const auto entry = [&](int i) { return !kPairs ? w[i] : k ? w[i] & 0xFFFF0000u : w[i] << 16; };
 #pragma unroll
         for (int v = 0; v < kLen; v += 16) {
             u32x4 q;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                q[e] = pack4(entry(v + 4 * e), entry(v + 4 * e + 1), entry(v + 4 * e + 2), entry(v + 4 * e + 3));
+                q[e] = pack_words(entry(v + 4 * e), entry(v + 4 * e + 1), entry(v + 4 * e + 2), entry(v + 4 * e + 3), inv);
             *reinterpret_cast<u32x4*>(out + (c + k) * kOut + kLen * part + v) = q;
         }
         if (part == 0 && cb * 128 + c + k < cols) scales_t[rb * cols + cb * 128 + c + k] = (uint8_t)(s + 127);
@@ -135,16 +133,21 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X
     }
 }
 
-// First two set bits of a group's four mask bits, as the four bits of its
-// metadata (unused slots point at a free position), and its two values (16 bits).
-__device__ __forceinline__ uint32_t take24(uint32_t bits, uint32_t q, uint32_t* v, int* over) {
+// What a group's four mask bits ask for: in the low half the byte permutation that takes
+// its first two kept values (0x0C: a zero byte for an unused slot), in bits 16..19 its
+// metadata (unused slots point at a free position), in bit 31 whether more than two are kept.
+__device__ __forceinline__ uint32_t group_entry(uint32_t bits) {
     const uint32_t rest = bits & (bits - 1u);
     const uint32_t p0 = bits ? (uint32_t)__builtin_ctz(bits) : 0u;
     const uint32_t p1 = rest ? (uint32_t)__builtin_ctz(rest) : (bits ? (p0 == 3u ? 2u : 3u) : 1u);
-    const uint32_t v0 = bits ? (q >> (8 * p0)) & 0xFFu : 0u, v1 = rest ? (q >> (8 * p1)) & 0xFFu : 0u;
-    *v = v0 | (v1 << 8);
-    *over += (rest & (rest - 1u)) != 0u;
-    return p0 | (p1 << 2);
+    return (bits ? p0 : 0x0Cu) | ((rest ? p1 : 0x0Cu) << 8) | ((p0 | (p1 << 2)) << 16) |
+           ((rest & (rest - 1u)) ? 0x80000000u : 0u);
+}
+// Two groups' values (entries a and b of the table) as one word.
+__device__ __forceinline__ uint32_t take_two(uint32_t a, uint32_t qa, uint32_t b, uint32_t qb) {
+    // the selectors' upper bytes are the table's other fields: those bytes are not used
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(0u, qb, b & 0xFFFFu), __builtin_amdgcn_perm(0u, qa, a & 0xFFFFu),
+                                 0x05040100u);
 }
 
 // One workgroup per 128 x 128 tile of one matrix.  The tile's kept entries
@@ -163,7 +166,7 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     __shared__ __attribute__((aligned(16))) uint8_t out[128 * kOut];
     __shared__ __attribute__((aligned(16))) uint16_t out_meta[128 * 8];
     __shared__ uint32_t bits[128][5];  // mask words of the tile's rows (padded against bank conflicts)
-    __shared__ uint32_t wmax[4];
+    __shared__ uint32_t wmax[4], table[16];
     const int64_t cblocks = (cols + 127) / 128, rblocks = (rows + 127) / 128;
     const int64_t per = rblocks * cblocks;
     const int64_t mat = blockIdx.x / per, t = blockIdx.x - mat * per;
@@ -172,16 +175,13 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     const int tid = threadIdx.x, l = tid & 15;
     W += mat * stride;
     mask += mat * rows * wpr;
-    T raw[8][8];
+    if (tid < 16) table[tid] = group_entry((uint32_t)tid);
+    Eight<T> raw[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int64_t r = rb * 128 + 16 * p + (tid >> 4);
-        if (r < rows) {
-            load8(W + r * ld, cb * 128 + 8 * l, cols, vec, raw[p]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) raw[p][i] = (T)0;
-        }
+        if (r < rows) raw[p].load(W + r * ld, cb * 128 + 8 * l, cols, vec);
+        else raw[p].clear();
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -199,12 +199,13 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     uint32_t m = 0u;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const uint32_t keep = bits[16 * p + (tid >> 4)][l >> 2] >> (8 * (l & 3));
+        raw[p].keep(bits[16 * p + (tid >> 4)][l >> 2] >> (8 * (l & 3)));
+        m = max(m, raw[p].magnitude());
+    }
+    if (__any(m >= kSpecial)) {
+        m = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (!((keep >> i) & 1u)) raw[p][i] = (T)0;
-            m = max(m, finite_magnitude(widen(raw[p][i])));
-        }
+        for (int p = 0; p < 8; ++p) m = max(m, raw[p].finite_only());
     }
     m = max16(m);
 #pragma unroll
@@ -218,26 +219,24 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     for (int p = 0; p < 8; ++p) {
         const int lr = 16 * p + (tid >> 4);
         const int64_t r = rb * 128 + lr;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = scaled(widen(raw[p][i]), inv);
-        const uint32_t q0 = pack4(y[0], y[1], y[2], y[3]), q1 = pack4(y[4], y[5], y[6], y[7]);
+        const u32x2 q = raw[p].quantised(inv);
         if (values != nullptr) {  // uniform
             const uint32_t keep = bits[lr][l >> 2] >> (8 * (l & 3));
-            uint32_t v0, v1;
-            const uint32_t n0 = take24(keep & 15u, q0, &v0, &over), n1 = take24((keep >> 4) & 15u, q1, &v1, &over);
+            const uint32_t g0 = table[keep & 15u], g1 = table[(keep >> 4) & 15u];
+            over += (int)(g0 >> 31) + (int)(g1 >> 31);
+            const uint32_t n0 = (g0 >> 16) & 15u, n1 = (g1 >> 16) & 15u;
             uint32_t word = (n0 | (n1 << 4)) << (8 * (l & 3));  // four lanes share a word
             word |= (uint32_t)__shfl_xor(word, 1, 64);
             word |= (uint32_t)__shfl_xor(word, 2, 64);
             if (r < rows) {
                 const int64_t at = (mat * rows + r) * cblocks + cb;
-                *reinterpret_cast<uint32_t*>(values + at * 64 + 4 * l) = v0 | (v1 << 16);
+                *reinterpret_cast<uint32_t*>(values + at * 64 + 4 * l) = take_two(g0, q.x, g1, q.y);
                 if ((l & 3) == 0) meta[at * 4 + (l >> 2)] = word;
             }
         }
         if (values_t != nullptr) {
-            *reinterpret_cast<uint32_t*>(&q8[lr * kLd + 8 * l]) = q0;
-            *reinterpret_cast<uint32_t*>(&q8[lr * kLd + 8 * l + 4]) = q1;
+            *reinterpret_cast<uint32_t*>(&q8[lr * kLd + 8 * l]) = q.x;
+            *reinterpret_cast<uint32_t*>(&q8[lr * kLd + 8 * l + 4]) = q.y;
         }
     }
     if (over && bad != nullptr) atomicAdd(bad, over);
@@ -249,28 +248,38 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     __syncthreads();
     over = 0;
     const int cq = tid & 31, part = tid >> 5;  // four columns, 16 rows
-    uint32_t v[4][2] = {}, mw[4] = {};
+    uint32_t v[4][2], mw[4] = {};
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        uint32_t q[4], kept = 0u;
+    for (int g2 = 0; g2 < 4; g2 += 2) {
+        uint32_t col[2][4], entry[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 16 * part + 4 * g + i;
-            q[i] = *reinterpret_cast<const uint32_t*>(&q8[r * kLd + 4 * cq]);
-            kept |= ((bits[r][cq >> 3] >> (4 * (cq & 7))) & 15u) << (4 * i);
+        for (int g = 0; g < 2; ++g) {
+            uint32_t q[4], kept = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * part + 4 * (g2 + g) + i;
+                q[i] = *reinterpret_cast<const uint32_t*>(&q8[r * kLd + 4 * cq]);
+                kept |= ((bits[r][cq >> 3] >> (4 * (cq & 7))) & 15u) << (4 * i);
+            }
+            // bytes of four rows to bytes of four columns
+            const uint32_t a = __builtin_amdgcn_perm(q[1], q[0], 0x05010400u);
+            const uint32_t b = __builtin_amdgcn_perm(q[3], q[2], 0x05010400u);
+            const uint32_t c = __builtin_amdgcn_perm(q[1], q[0], 0x07030602u);
+            const uint32_t d = __builtin_amdgcn_perm(q[3], q[2], 0x07030602u);
+            col[g][0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            col[g][1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+            col[g][2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+            col[g][3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = (kept >> j) & 0x1111u;  // this column's bits, one in each nibble
+                entry[g][j] = table[(x | (x >> 3) | (x >> 6) | (x >> 9)) & 15u];
+                over += (int)(entry[g][j] >> 31);
+                mw[j] |= ((entry[g][j] >> 16) & 15u) << (4 * (g2 + g));
+            }
         }
-        // bytes of four rows to bytes of four columns
-        const uint32_t a = __builtin_amdgcn_perm(q[1], q[0], 0x05010400u), b = __builtin_amdgcn_perm(q[3], q[2], 0x05010400u);
-        const uint32_t c = __builtin_amdgcn_perm(q[1], q[0], 0x07030602u), d = __builtin_amdgcn_perm(q[3], q[2], 0x07030602u);
-        const uint32_t col[4] = {__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(b, a, 0x07060302u),
-                                 __builtin_amdgcn_perm(d, c, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t x = (kept >> j) & 0x1111u;  // this column's bits, one in each nibble
-            uint32_t two;
-            mw[j] |= take24((x | (x >> 3) | (x >> 6) | (x >> 9)) & 15u, col[j], &two, &over) << (4 * g);
-            v[j][g >> 1] |= two << (16 * (g & 1));
-        }
+        for (int j = 0; j < 4; ++j) v[j][g2 >> 1] = take_two(entry[0][j], col[0][j], entry[1][j], col[1][j]);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
