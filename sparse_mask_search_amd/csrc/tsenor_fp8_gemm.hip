@@ -234,6 +234,9 @@ constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside
 // rows 8 i0 + 4h + i1 in register 4 i0 + i1.  The dense instruction takes any order of
 // the entries that is the same for both operands.
 
+// 2^e for e <= 127; 0 below 2^-126.
+__device__ __forceinline__ float power(int e) { return bits_float(e < -126 ? 0u : (uint32_t)(127 + e) << 23); }
+
 // Y = X A^T (A on the rows of the instruction).
 template <int TM, int TN, int WM, int WN, int R, class TY>
 __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
@@ -278,6 +281,12 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
 
+    // Each column's sums are held in units of 2^unit[b]: the scale product of the last block
+    // that went in.
+    int unit[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) unit[b] = 0;
+
     // loads of step t into `buf` (behind the last step: the last step again, into a
     // buffer that nobody reads any more)
     auto issue = [&](int t, Buffer& buf) {
@@ -300,7 +309,21 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
                                : min(l & (TM / 128 > 1 ? 1 : 0), (int)(((m - 1) >> 7) - (m0 >> 7))) * (uint32_t)kb;
         dma_byte(sbase + s * sstep, so, lds_offset(buf.scale + sdst));
     };
-    auto step = [&](int t, Buffer& buf, Buffer& next) {
+    i32x8 bv[2][TB];
+    i32x4 av[2][2];
+    int idx[2][2];
+    int u[TB];  // the block's scale product, as the sum of both bytes
+    auto read_a = [&](int a, const Buffer& buf) {  // 32 rows of A into the set a & 1
+        const int l = lane, lh = l >> 5, lr = l & 31;
+        const int r = (TM / WM) * wm + 32 * a + lr, sw = (lr >> 2) & 3;
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc) {
+            av[a & 1][kc] = __builtin_bit_cast(i32x4, buf.a[4 * r + ((2 * kc + lh) ^ sw)]);
+            idx[a & 1][kc] = (int)buf.meta[4 * r + 2 * kc + lh];
+        }
+    };
+    // Step t up to its first operands.
+    auto begin = [&](int t, Buffer& buf, Buffer& next) {
         // this step's loads have landed when at most the next R - 2 steps' are outstanding,
         // and this wave's LDS reads of the step before are done; after the barrier that holds
         // for all waves, so the buffer that step t + R - 1 fills is free
@@ -309,56 +332,99 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         issue(t + R - 1, next);
-        const int l = opaque(lane), lh = l >> 5, lr = l & 31;
-        float f[TB];
-        i32x8 bv[2][TB];
+        const int l = lane, lh = l >> 5, lr = l & 31;
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
             const int r = (TN / WN) * wn + 32 * b + lr, sw = (lr >> 1) & 7;
-            f[b] = scale_product((int)buf.scale[r], (int)buf.scale[TN + (TM > 128 ? wm : 0)]);
+            u[b] = (int)buf.scale[r] + (int)buf.scale[TN + (TM > 128 ? wm : 0)];
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc)
                 bv[kc][b] = join(buf.x[8 * r + ((4 * kc + lh) ^ sw)], buf.x[8 * r + ((4 * kc + 2 + lh) ^ sw)]);
         }
-        // Tile i+1 runs on the matrix cores while tile i is scaled and added; the operands of
-        // A's next 32 rows are read a tile ahead.  The fences keep the compiler from having
-        // more partial tiles alive than the registers hold.
-        i32x4 av[2][2];
-        int idx[2][2];
-        f32x16 d[2];
-        auto read_a = [&](int a) {
-            const int r = (TM / WM) * wm + 32 * a + lr, sw = (lr >> 2) & 3;
+        read_a(0, buf);
+    };
+    // The sums change to this block's unit and the block is added in place: 16
+    // multiplications a tile, where a fresh partial tile takes 16 clears and 16 multiply-adds.
+    // No sum passes 2^60 times what its largest block can hold.
+    auto add_near = [&](const Buffer& buf) {
+        float f[TB];
 #pragma unroll
-            for (int kc = 0; kc < 2; ++kc) {
-                av[a & 1][kc] = __builtin_bit_cast(i32x4, buf.a[4 * r + ((2 * kc + lh) ^ sw)]);
-                idx[a & 1][kc] = (int)buf.meta[4 * r + 2 * kc + lh];
-            }
-        };
-        auto multiply = [&](int i) {
-            const int a = (i / TB) & 1, b = i % TB;
+        for (int b = 0; b < TB; ++b) {
+            f[b] = power(unit[b] - u[b]);
+            unit[b] = u[b];
+        }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) d[i & 1][e] = 0.f;
-            d[i & 1] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a][0], bv[0][b], d[i & 1], idx[a][0], 0, 0);
-            d[i & 1] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a][1], bv[1][b], d[i & 1], idx[a][1], 0, 0);
-        };
-        read_a(0);
-        multiply(0);
+        for (int a = 0; a < TA; ++a) {
+            if (a + 1 < TA) read_a(a + 1, buf);
 #pragma unroll
-        for (int i = 0; i < TA * TB; ++i) {
-            if (i % TB == 0 && i / TB + 1 < TA) read_a(i / TB + 1);
-            if (i + 1 < TA * TB) multiply(i + 1);
+            for (int b = 0; b < TB; ++b)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                acc[i / TB][i % TB][e] = __builtin_fmaf(d[i & 1][e], f[i % TB], acc[i / TB][i % TB][e]);
+                for (int e = 0; e < 16; ++e) acc[a][b][e] *= f[b];
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+                for (int b = 0; b < TB; ++b)
+                    acc[a][b] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a & 1][kc], bv[kc][b], acc[a][b],
+                                                                            idx[a & 1][kc], 0, 0);
             __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // Any block: the sums keep the larger unit, and the block is summed apart and scaled down.
+    auto add_far = [&](const Buffer& buf) {
+        float f[TB], g[TB];
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+            const int to = max(unit[b], u[b]);
+            f[b] = power(unit[b] - to);
+            g[b] = power(u[b] - to);
+            unit[b] = to;
+        }
+#pragma unroll
+        for (int a = 0; a < TA; ++a) {
+            if (a + 1 < TA) read_a(a + 1, buf);
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                f32x16 d;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) d[e] = 0.f;
+#pragma unroll
+                for (int kc = 0; kc < 2; ++kc)
+                    d = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a & 1][kc], bv[kc][b], d, idx[a & 1][kc], 0, 0);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[a][b][e] = __builtin_fmaf(d[e], g[b], acc[a][b][e] * f[b]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
 #pragma unroll
     for (int t = 0; t < R - 1; ++t) issue(t, ring[t]);
+    // Whether all blocks of each of the wave's columns are within 2^60 of each other.  (The
+    // waves stay in step: one barrier a step in either loop.)
+    bool near = true;
+    {
+        const uint8_t* as = scales + ((m0 + (TM / WM) * wm) >> 7 < (m + 127) >> 7 ? (m0 + (TM / WM) * wm) >> 7 : m0 >> 7) * kb;
+        const uint8_t* x = xs + min(n0 + (TN / WN) * wn + (lane & (TN / WN - 1)), n - 1);
+        int lo = 1 << 16, hi = 0;
+#pragma unroll 16
+        for (int t = 0; t < steps; ++t) {
+            const int v = (int)x[t * n] + (int)as[t];
+            lo = min(lo, v);
+            hi = max(hi, v);
+        }
+        near = __all(hi - lo <= 60);
+    }
     int cur = 0;
-    for (int t = 0; t < steps; ++t) {
-        step(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
-        cur = cur == R - 1 ? 0 : cur + 1;
+    const auto next_of = [](int v) { return v == R - 1 ? 0 : v + 1; };
+    if (near) {
+        for (int t = 0; t < steps; ++t, cur = next_of(cur)) {
+            begin(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
+            add_near(ring[cur]);
+        }
+    } else {
+        for (int t = 0; t < steps; ++t, cur = next_of(cur)) {
+            begin(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
+            add_far(ring[cur]);
+        }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
@@ -369,9 +435,12 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
 #pragma unroll
         for (int a = 0; a < TA; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                store4(y, m0 + (TM / WM) * wm + 32 * a + 8 * i + 4 * h, m, yvec,
-                       f32x4{acc[a][b][4 * i], acc[a][b][4 * i + 1], acc[a][b][4 * i + 2], acc[a][b][4 * i + 3]});
+            for (int i = 0; i < 4; ++i) {
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[a][b][4 * i + e], unit[b] - 254);
+                store4(y, m0 + (TM / WM) * wm + 32 * a + 8 * i + 4 * h, m, yvec, v);
+            }
     }
 }
 
