@@ -241,13 +241,6 @@ __device__ __forceinline__ void tile_of(int64_t bid, int64_t tiles_m, int64_t ti
     tn = r / gm;
 }
 
-// The same value, unknown to the compiler: what is computed from it inside a loop
-// stays there, where it costs an instruction, and not in a register across the loop.
-__device__ __forceinline__ int opaque(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
-
 // Metadata of four blocks of a row at once.  A block's four words are for the four lane
 // groups q = lane / 16; read one by one, a load brings 16 bytes of each of 16 rows and costs
 // the address unit as much as one that brings 64.  So lane group g reads all four words of

@@ -287,27 +287,37 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
 #pragma unroll
     for (int b = 0; b < TB; ++b) unit[b] = 0;
 
-    // loads of step t into `buf` (behind the last step: the last step again, into a
+    // load number j of step t into `buf` (behind the last step: the last step again, into a
     // buffer that nobody reads any more)
-    auto issue = [&](int t, Buffer& buf) {
+    constexpr int kLoads = QX + 2 * QA + 1;
+    auto load = [&](int j, int t, Buffer& buf) {
         const int64_t s = t < steps ? t : steps - 1;
-        const int l = opaque(lane);
-#pragma unroll
-        for (int j = 0; j < QX; ++j) {
+        const int l = lane;
+        if (j < QX) {
             const int r = 8 * (wave * QX + j) + (l >> 3), c = l & 7;
             dma16(xbase + 128 * s, __umul24(min(r, xlast), (uint32_t)ldx) + 16 * (c ^ ((r >> 1) & 7)),
                   lds_offset(buf.x + 64 * (wave * QX + j)));
-        }
-#pragma unroll
-        for (int j = 0; j < QA; ++j) {
-            const int r = 16 * (wave * QA + j) + (l >> 2), c = l & 3;
+        } else if (j < QX + 2 * QA) {
+            const int i = (j - QX) >> 1, r = 16 * (wave * QA + i) + (l >> 2), c = l & 3;
             const uint32_t row = __umul24(min(r, alast), (uint32_t)kb);
-            dma16(abase + 64 * s, 64 * row + 16 * (c ^ ((r >> 2) & 3)), lds_offset(buf.a + 64 * (wave * QA + j)));
-            dma4(mbase + 16 * s, 16 * row + 4 * c, lds_offset(buf.meta + 64 * (wave * QA + j)));
+            if (((j - QX) & 1) == 0)
+                dma16(abase + 64 * s, 64 * row + 16 * (c ^ ((r >> 2) & 3)), lds_offset(buf.a + 64 * (wave * QA + i)));
+            else
+                dma4(mbase + 16 * s, 16 * row + 4 * c, lds_offset(buf.meta + 64 * (wave * QA + i)));
+        } else {
+            const uint32_t so = xw ? min(64 * wave + l, xlast)
+                                   : min(l & (TM / 128 > 1 ? 1 : 0), (int)(((m - 1) >> 7) - (m0 >> 7))) * (uint32_t)kb;
+            dma_byte(sbase + s * sstep, so, lds_offset(buf.scale + sdst));
         }
-        const uint32_t so = xw ? min(64 * wave + l, xlast)
-                               : min(l & (TM / 128 > 1 ? 1 : 0), (int)(((m - 1) >> 7) - (m0 >> 7))) * (uint32_t)kb;
-        dma_byte(sbase + s * sstep, so, lds_offset(buf.scale + sdst));
+    };
+    // part a of TA of the loads of step t: spread over a step, they do not stall all waves on
+    // the address unit at once (8192 x 28672 x 8192: 1610 -> 1555 us); with two buffers they are
+    // needed in the next step and go out first (2048 x 4096 x 4096: 43 us against 49)
+    auto load_part = [&](int a, int t, Buffer& buf) {
+        constexpr int kParts = R > 2 ? TA : 1;
+        if (a >= kParts) return;
+#pragma unroll
+        for (int j = a * kLoads / kParts; j < (a + 1) * kLoads / kParts; ++j) load(j, t, buf);
     };
     i32x8 bv[2][TB];
     i32x4 av[2][2];
@@ -323,15 +333,14 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
         }
     };
     // Step t up to its first operands.
-    auto begin = [&](int t, Buffer& buf, Buffer& next) {
+    auto begin = [&](const Buffer& buf) {
         // this step's loads have landed when at most the next R - 2 steps' are outstanding,
         // and this wave's LDS reads of the step before are done; after the barrier that holds
-        // for all waves, so the buffer that step t + R - 1 fills is free
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((R - 2) * (QX + 2 * QA + 1)) : "memory");
+        // for all waves, so the buffer that step t + R - 1 fills (during this one) is free
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((R - 2) * kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        issue(t + R - 1, next);
         const int l = lane, lh = l >> 5, lr = l & 31;
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
@@ -346,7 +355,7 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
     // The sums change to this block's unit and the block is added in place: 16
     // multiplications a tile, where a fresh partial tile takes 16 clears and 16 multiply-adds.
     // No sum passes 2^60 times what its largest block can hold.
-    auto add_near = [&](const Buffer& buf) {
+    auto add_near = [&](int t, const Buffer& buf, Buffer& free) {
         float f[TB];
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
@@ -355,6 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
         }
 #pragma unroll
         for (int a = 0; a < TA; ++a) {
+            if (R == 2) load_part(a, t + R - 1, free);
             if (a + 1 < TA) read_a(a + 1, buf);
 #pragma unroll
             for (int b = 0; b < TB; ++b)
@@ -366,11 +376,12 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
                 for (int b = 0; b < TB; ++b)
                     acc[a][b] = __builtin_amdgcn_smfmac_f32_32x32x64_fp8_fp8(av[a & 1][kc], bv[kc][b], acc[a][b],
                                                                             idx[a & 1][kc], 0, 0);
+            if (R > 2) load_part(a, t + R - 1, free);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     // Any block: the sums keep the larger unit, and the block is summed apart and scaled down.
-    auto add_far = [&](const Buffer& buf) {
+    auto add_far = [&](int t, const Buffer& buf, Buffer& free) {
         float f[TB], g[TB];
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
@@ -382,6 +393,7 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
 #pragma unroll
         for (int a = 0; a < TA; ++a) {
             if (a + 1 < TA) read_a(a + 1, buf);
+            load_part(a, t + R - 1, free);
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
                 f32x16 d;
@@ -397,7 +409,9 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
         }
     };
 #pragma unroll
-    for (int t = 0; t < R - 1; ++t) issue(t, ring[t]);
+    for (int t = 0; t < R - 1; ++t)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) load(j, t, ring[t]);
     // Whether all blocks of each of the wave's columns are within 2^60 of each other.  (The
     // waves stay in step: one barrier a step in either loop.)
     bool near = true;
@@ -417,13 +431,13 @@ __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
     const auto next_of = [](int v) { return v == R - 1 ? 0 : v + 1; };
     if (near) {
         for (int t = 0; t < steps; ++t, cur = next_of(cur)) {
-            begin(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
-            add_near(ring[cur]);
+            begin(ring[cur]);
+            add_near(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
         }
     } else {
         for (int t = 0; t < steps; ++t, cur = next_of(cur)) {
-            begin(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
-            add_far(ring[cur]);
+            begin(ring[cur]);
+            add_far(t, ring[cur], ring[cur == 0 ? R - 1 : cur - 1]);
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
