@@ -48,26 +48,27 @@ def _placed(fn):
     @functools.wraps(fn)
     def call(x, *args, stream=None, **kw):
         torch = _lib._torch()
-        t = x if isinstance(x, torch.Tensor) else getattr(x, "values", None)
+        t = x.values if isinstance(x, (DenseFp8, Sparse24Fp8)) else x
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{fn.__name__} needs CUDA (HIP) torch tensors")
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-            with torch.cuda.stream(stream):
+        device = t.device
+        if stream is None and device.index == torch.cuda.current_device():
+            return fn(torch, x, *args, **kw)
+        if stream is None:
+            with torch.cuda.device(device):
                 return fn(torch, x, *args, **kw)
-        if t.device.index != torch.cuda.current_device():
-            with torch.cuda.device(t.device):
-                return fn(torch, x, *args, **kw)
-        return fn(torch, x, *args, **kw)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return fn(torch, x, *args, **kw)
     return call
 
 
-def _run(torch, where, t, fn, *args):
+def _run(torch, where, device, fn, *args):
     # the handle of the current stream; the public way builds a Stream object first (1.8 us,
     # a sixth of a small call)
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    stream = raw(t.device.index) if raw else torch.cuda.current_stream(t.device).cuda_stream
+    stream = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
     st = fn(*args, stream)
     if st != 0:
         raise TsenorError(st, where)
@@ -124,10 +125,11 @@ def _sparse(torch, a, device, name, lead, rows=None):
     return rows
 
 
-def _out(torch, out, shape, dtype, device):
-    """A fresh result, or `out` after checking it."""
+def _out(torch, out, shape, dtype, near):
+    """A fresh result on the device of `near`, or `out` after checking it."""
     if out is None:
-        return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
+        return near.new_empty(shape, dtype=dtype or torch.bfloat16)
+    device = near.device
     _matrix(torch, out, "out")
     if tuple(out.shape) != shape or out.device != device or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must be a tensor of shape {shape} on {device}"
@@ -137,23 +139,24 @@ def _out(torch, out, shape, dtype, device):
     return out
 
 
-def _new_dense(torch, rows, k, device):
-    return DenseFp8(torch.empty((rows, _pad(k)), dtype=torch.float8_e4m3fn, device=device),
-                    torch.empty((_blocks(k), rows), dtype=torch.float8_e8m0fnu, device=device), k)
-
-
 def _quant(torch, X, by_rows, by_cols):
     _matrix(torch, X, "X")
     dt = _float_type(torch, X, "X")
     rows, cols = X.shape
     if cols == 0:
         raise ValueError("X has no columns")
-    a = _new_dense(torch, rows, cols, X.device) if by_rows else None
-    b = _new_dense(torch, cols, rows, X.device) if by_cols else None
+    new, e4m3, e8m0 = X.new_empty, torch.float8_e4m3fn, torch.float8_e8m0fnu
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    a = b = av = as_ = bv = bs = None
+    if by_rows:
+        a = DenseFp8(new((rows, cb * 128), dtype=e4m3), new((cb, rows), dtype=e8m0), cols)
+        av, as_ = a.values.data_ptr(), a.scales.data_ptr()
+    if by_cols:
+        b = DenseFp8(new((cols, rb * 128), dtype=e4m3), new((rb, cols), dtype=e8m0), rows)
+        bv, bs = b.values.data_ptr(), b.scales.data_ptr()
     if rows:
-        _run(torch, "tsenor_quant_fp8", X, lib().tsenor_quant_fp8, X.data_ptr(), dt, rows, cols, _ld(X),
-             a and a.values.data_ptr(), a and a.scales.data_ptr(),
-             b and b.values.data_ptr(), b and b.scales.data_ptr())
+        _run(torch, "tsenor_quant_fp8", X.device, lib().tsenor_quant_fp8, X.data_ptr(), dt, rows, cols,
+             _ld(X), av, as_, bv, bs)
     return a, b
 
 
@@ -181,15 +184,15 @@ def _compress(torch, W, mask, by_rows, by_cols):
 
     def new(r, k):
         b = _blocks(k)
-        return Sparse24Fp8(torch.empty((*lead, r, 64 * b), dtype=torch.float8_e4m3fn, device=dev),
-                           torch.empty((*lead, r, 4 * b), dtype=torch.int32, device=dev),
-                           torch.empty((*lead, _blocks(r), b), dtype=torch.float8_e8m0fnu, device=dev), k)
+        return Sparse24Fp8(W.new_empty((*lead, r, 64 * b), dtype=torch.float8_e4m3fn),
+                           W.new_empty((*lead, r, 4 * b), dtype=torch.int32),
+                           W.new_empty((*lead, _blocks(r), b), dtype=torch.float8_e8m0fnu), k)
 
     a = new(rows, cols) if by_rows else None
     t = new(cols, rows) if by_cols else None
     bad_a, bad_t = torch.zeros((2, 1), dtype=torch.int32, device=dev).unbind()
     if not stacked or W.shape[0]:
-        _run(torch, "tsenor_compress24_fp8", W, lib().tsenor_compress24_fp8, W.data_ptr(), dt,
+        _run(torch, "tsenor_compress24_fp8", dev, lib().tsenor_compress24_fp8, W.data_ptr(), dt,
              W.shape[0] if stacked else 1, W.stride(0) if stacked else 0, rows, cols, _ld(W),
              mask.data_ptr(), a and a.values.data_ptr(), a and a.meta.data_ptr(),
              a and a.scales.data_ptr(), t and t.values.data_ptr(), t and t.meta.data_ptr(),
@@ -231,7 +234,7 @@ def spmm24_fp8(torch, X, A, out=None, dtype=None):
     m = _sparse(torch, A, device, "A", ())
     if A.k != k:
         raise ValueError(f"X has {k} columns, A has {A.k}")
-    out = _out(torch, out, (n, m), dtype, device)
+    out = _out(torch, out, (n, m), dtype, A.values)
     yt = _float_type(torch, out, "out")
     if n == 0 or m == 0:
         return out
@@ -240,7 +243,7 @@ def spmm24_fp8(torch, X, A, out=None, dtype=None):
     else:
         q = X if ready else _quant(torch, X, True, False)[0]
         x, xtype, xs, ldx = q.values, E4M3, q.scales.data_ptr(), q.values.shape[1]
-    _run(torch, "tsenor_spmm24_fp8", x, lib().tsenor_spmm24_fp8, x.data_ptr(), xtype, xs, n, ldx,
+    _run(torch, "tsenor_spmm24_fp8", device, lib().tsenor_spmm24_fp8, x.data_ptr(), xtype, xs, n, ldx,
          A.values.data_ptr(), A.meta.data_ptr(), A.scales.data_ptr(), m, k, out.data_ptr(), yt, _ld(out))
     return out
 
@@ -251,17 +254,19 @@ def gemm_fp8(torch, A, B, mask=None, out=None, dtype=None):
     words [p, ceil(q / 32)]) the removed entries are 0 (tsenor_gemm_fp8).  The
     masked weight gradient of Y = X W^T is
     gemm_fp8(quant_fp8(dY, transpose=True), quant_fp8(X, transpose=True), mask)."""
+    if not isinstance(A, DenseFp8):
+        raise TypeError("A must be a DenseFp8 operand (quant_fp8)")
     device = A.values.device
     p, q = _dense(torch, A, device, "A"), _dense(torch, B, device, "B")
     if A.k != B.k:
         raise ValueError(f"A has {A.k} columns, B has {B.k}")
     if mask is not None:
         _part(torch, mask, torch.int32, (p, (q + 31) // 32), device, "mask")
-    out = _out(torch, out, (p, q), dtype, device)
+    out = _out(torch, out, (p, q), dtype, A.values)
     ct = _float_type(torch, out, "out")
     if p == 0 or q == 0:
         return out
-    _run(torch, "tsenor_gemm_fp8", out, lib().tsenor_gemm_fp8, A.values.data_ptr(), A.scales.data_ptr(),
+    _run(torch, "tsenor_gemm_fp8", device, lib().tsenor_gemm_fp8, A.values.data_ptr(), A.scales.data_ptr(),
          p, B.values.data_ptr(), B.scales.data_ptr(), q, A.k,
          None if mask is None else mask.data_ptr(), out.data_ptr(), ct, _ld(out))
     return out
@@ -285,12 +290,12 @@ def moe24_fp8(torch, x, router, gate, up, down, topk: int, out=None, return_rout
     _sparse(torch, down, device, "down", (experts,), d)
     if gate.k != d or up.k != d or down.k != f:
         raise ValueError(f"gate and up must have {d} columns, down {f}")
-    out = _out(torch, out, (n, d), torch.bfloat16, device)
+    out = _out(torch, out, (n, d), torch.bfloat16, x)
     ids = torch.empty((n, topk), dtype=torch.int32, device=device) if return_routing else None
     weights = torch.empty((n, topk), dtype=torch.float32, device=device) if return_routing else None
     size = lib().tsenor_moe24_fp8_workspace(n, d, f, experts, topk)
     work = torch.empty(size, dtype=torch.uint8, device=device)
-    _run(torch, "tsenor_moe24_fp8", x, lib().tsenor_moe24_fp8, x.data_ptr(), n, _ld(x), d,
+    _run(torch, "tsenor_moe24_fp8", device, lib().tsenor_moe24_fp8, x.data_ptr(), n, _ld(x), d,
          router.data_ptr(), _ld(router), experts, topk, gate.values.data_ptr(), gate.meta.data_ptr(),
          gate.scales.data_ptr(), up.values.data_ptr(), up.meta.data_ptr(), up.scales.data_ptr(),
          down.values.data_ptr(), down.meta.data_ptr(), down.scales.data_ptr(), f, work.data_ptr(), size,

@@ -5,7 +5,7 @@
 //   hidden  per chosen expert and some rows of gate and up: both products, silu, product;
 //   down    per chosen expert and some rows of down: what each of its tokens gains;
 //   sum     a token's gains, weighted, in the order of its choices.
-// Reading the chosen experts' weights bounds the layer, so a workgroup's eight
+// Reading the chosen experts' weights bounds the layer, so a workgroup's four
 // waves share the reduction out in stretches and keep several blocks' loads in
 // flight; the waves' sums meet in LDS in wave order, without atomics.
 // The hidden entries are kept as the sum of two bf16 numbers (16 fraction bits;
@@ -37,7 +37,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kMaxTokens = 64, kMaxTop = 16;
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;  // of the hidden and down workgroups
 
 // Where entry k of a row of activations is kept: eight entries stay together; within
 // their block of 128, load i = 2j + (half) of lane group q finds them at 8 (4i + q).
@@ -462,14 +462,15 @@ int launch_moe24_fp8(const MoeJob& a, void* stream) {
     hipLaunchKernelGGL(route, dim3(1), dim3(64 * kRouteWaves), 0, s, a, (int)groups);
     e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    // Rows of a workgroup: 64, so that a token's activations are read once for four tiles, or
-    // 16 where that would leave too few workgroups.  Measured (us) with 64 / 16 rows: hidden, one
-    // token, 6 experts, 2048 x 1408: 13.3 / 11.4; 33 tokens, 16 experts, 4096 x 2048: 38 / 43;
-    // down: 5.5 / 7.6 and 30 / 54.
+    // Rows of a workgroup: several tiles of 16, so that a token's activations are read once for
+    // all of them, unless too few workgroups would be left.  Measured (us, four waves; eight are
+    // slower by 0 to 20%, as their stretches end inside the four blocks whose metadata one load
+    // brings) with 16 / 32 / 64 rows: hidden, one token, 6 experts, 2048 x 1408: 9.9 / 11.6 / 12.7;
+    // 33 tokens, 16 experts, 4096 x 2048: 44 / 39 / 41; down: 6.8 / 6.0 / 5.8 and 49 / 32 / 25.
     const auto tiles = [&](int64_t length, int rows) { return groups * ((length + rows - 1) / rows); };
     const dim3 threads(64 * kWaves);
-    if (tiles(a.f, 64) >= 256)
-        hipLaunchKernelGGL(moe_hidden_kernel<4>, dim3((unsigned)tiles(a.f, 64)), threads, 0, s, a);
+    if (tiles(a.f, 32) >= 512)
+        hipLaunchKernelGGL(moe_hidden_kernel<2>, dim3((unsigned)tiles(a.f, 32)), threads, 0, s, a);
     else
         hipLaunchKernelGGL(moe_hidden_kernel<1>, dim3((unsigned)tiles(a.f, 16)), threads, 0, s, a);
     e = hipGetLastError();
