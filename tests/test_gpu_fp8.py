@@ -318,6 +318,46 @@ def test_spmm_nan_stays_in_its_row_and_extreme_scales(n):
     assert bool(torch.isnan(y[1][hit]).all()) and int(hit.sum()) > 0
 
 
+# Shapes that reach each tile size of the tiled kernels (256 x 256, 128 x 128, 128 x 64),
+# ragged in every dimension.
+TILED = [(4100, 4104, 260), (2900, 3012, 132), (1000, 4100, 388)]
+
+
+def exact_product(x, w):
+    """An integer-valued product on the GPU in fp64."""
+    import torch
+    return torch.from_numpy(x).cuda() @ torch.from_numpy(w).cuda().t()
+
+
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("n,m,k", TILED)
+def test_spmm_tiles_exact(n, m, k, far):
+    """far: some rows of X hold integers times 2^-80 in their first block and zeros (scale 1)
+    behind it, so that scales more than 2^60 apart meet in one row."""
+    import torch
+    say("spmm tiles", n, m, k, far)
+    rng = np.random.default_rng(n + m + k)
+    keep = np.tile(ref.random24(rng, 64, k), (-(-m // 64), 1))[:m]
+    w, wv = tensor(integers(rng, (m, k), 7) * powers_square(rng, m, k), "bf16")
+    xv = integers(rng, (n, k), 7) * powers(rng, n, k)
+    if far:
+        rows = rng.choice(n, 40, replace=False)
+        xv[rows, :128] *= 2.0 ** -80
+        xv[rows, 128:] = 0
+    x, xv = tensor(xv, "bf16")
+    A, bad = sms.compress24_fp8(w, words(keep))
+    buf = torch.full((n + 2, m + 4), 7.0, device="cuda")
+    y = buf[1:n + 1, 4:m + 4]
+    sms.spmm24_fp8(x, A, out=y)
+    yb = sms.spmm24_fp8(x, A)
+    sync()
+    assert int(bad.item()) == 0
+    assert torch.equal(y.double(), exact_product(xv, np.where(keep, wv, 0)))
+    assert torch.equal(yb, y.bfloat16())
+    y.fill_(7.0)
+    assert bool((buf == 7.0).all())
+
+
 def test_spmm_no_tokens():
     import torch
     rng = np.random.default_rng(2)
@@ -395,6 +435,27 @@ def test_gemm_exact(p, q, k):
     sync()
     assert np.array_equal(f64(c), av @ bv.T)
     assert torch.equal(cb, c.bfloat16())
+
+
+@pytest.mark.parametrize("p,q,k", [(4100, 4104, 261), (2900, 3011, 130), (1000, 4099, 389)])
+def test_gemm_tiles_exact(p, q, k):
+    import torch
+    say("gemm tiles", p, q, k)
+    rng = np.random.default_rng(p + q + k)
+    a, av = tensor(integers(rng, (p, k), 7) * powers(rng, p, k, 2), "bf16")
+    b, bv = tensor(integers(rng, (q, k), 7) * powers(rng, q, k, 2), "bf16")
+    keep = np.tile(rng.random((64, q)) < 0.5, (-(-p // 64), 1))[:p]
+    A, B = sms.quant_fp8(a), sms.quant_fp8(b)
+    buf = torch.full((p + 2, q + 4), 7.0, device="cuda")
+    c = buf[1:p + 1, 4:q + 4]
+    sms.gemm_fp8(A, B, mask=words(keep), out=c)
+    cb = sms.gemm_fp8(A, B)
+    sync()
+    want = exact_product(av, bv)
+    assert torch.equal(cb, want.float().bfloat16())
+    assert torch.equal(c.double(), want * torch.from_numpy(keep).cuda())
+    c.fill_(7.0)
+    assert bool((buf == 7.0).all())
 
 
 def test_gemm_no_tokens_gives_zeros():
@@ -574,7 +635,8 @@ def _moe_reference(xv, ids, wts, gate, up, down):
 
 @pytest.mark.parametrize("n,d,f,e,topk", [(1, 128, 128, 4, 2), (1, 260, 140, 8, 3), (2, 64, 36, 3, 1),
                                           (7, 516, 260, 16, 8), (17, 384, 132, 5, 5), (33, 256, 256, 4, 1),
-                                          (64, 132, 388, 8, 2), (64, 256, 128, 2, 2), (5, 128, 64, 200, 16)])
+                                          (64, 132, 388, 8, 2), (64, 256, 128, 2, 2), (5, 128, 64, 200, 16),
+                                          (3, 128, 32, 1, 1), (64, 64, 36, 512, 3), (24, 1028, 1400, 12, 6)])
 def test_moe(n, d, f, e, topk):
     import torch
     say("moe", n, d, f, e, topk)
