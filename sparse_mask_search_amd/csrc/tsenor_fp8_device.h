@@ -18,7 +18,6 @@ constexpr int kBlock = 128;  // entries that share a scale along a row
 
 __host__ __device__ __forceinline__ int64_t pad128(int64_t k) { return (k + 127) / 128 * 128; }
 
-__device__ __forceinline__ uint32_t float_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }
 
 __device__ __forceinline__ float widen(uint16_t b) { return bits_float((uint32_t)b << 16); }
@@ -74,21 +73,6 @@ __device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t co
         for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : (uint16_t)0;
     }
 }
-__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, bool vec,
-                                      float v[8]) {
-    if (vec && c + 8 <= cols) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(row + c);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(row + c + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.f;
-    }
-}
 
 // Eight neighbouring entries in registers, bf16 as four pairs.  Magnitudes order like the
 // bits below the sign, so a maximum needs no conversion; one of kSpecial or more tells of an
@@ -129,10 +113,18 @@ template <>
 struct Eight<uint16_t> {
     uint32_t w[4];
     __device__ __forceinline__ void load(const uint16_t* row, int64_t c, int64_t cols, bool vec) {
-        uint16_t v[8];
-        load8(row, c, cols, vec, v);
+        if (vec && c + 8 <= cols) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(row + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)v[2 * i] | ((uint32_t)v[2 * i + 1] << 16);
+            for (int i = 0; i < 4; ++i) w[i] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = c + 2 * i < cols ? row[c + 2 * i] : 0u;
+                const uint32_t hi = c + 2 * i + 1 < cols ? row[c + 2 * i + 1] : 0u;
+                w[i] = lo | (hi << 16);
+            }
+        }
     }
     __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
     __device__ __forceinline__ void keep(uint32_t bits) {  // bit i: entry i stays
@@ -163,10 +155,19 @@ template <>
 struct Eight<float> {
     uint32_t w[8];
     __device__ __forceinline__ void load(const float* row, int64_t c, int64_t cols, bool vec) {
-        float v[8];
-        load8(row, c, cols, vec, v);
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(row) + c;
+        if (vec && c + 8 <= cols) {
+            const u32x4 a = *reinterpret_cast<const u32x4*>(from);
+            const u32x4 b = *reinterpret_cast<const u32x4*>(from + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = float_bits(v[i]);
+            for (int i = 0; i < 4; ++i) {
+                w[i] = a[i];
+                w[4 + i] = b[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = c + i < cols ? from[i] : 0u;
+        }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll

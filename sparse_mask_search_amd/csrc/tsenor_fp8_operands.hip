@@ -158,6 +158,8 @@ __device__ __forceinline__ uint32_t take_two(uint32_t a, uint32_t qa, uint32_t b
 // numbers go to LDS, a thread turns 4 x 4 cells of them around with byte permutations, and
 // the compressed columns leave through LDS as whole lines.  11008 x 4096 bf16 both ways: 43 us
 // for 152 MB; some 1000 VALU instructions a thread keep it from the memory's rate.
+// 8192 x 8192 f32: 83 us for 361 MB.  The compressed columns take the tile's place in LDS (19.5 KB
+// in all against 29), which is worth 4 to 8%.
 template <class T>
 __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     const T* __restrict__ W, int64_t stride, int64_t rows, int64_t cols, int64_t ld, bool vec,
@@ -166,8 +168,9 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     uint8_t* __restrict__ scales_t, int* __restrict__ bad, int* __restrict__ bad_t) {
     constexpr int kLd = 132, kOut = 80;  // bytes of a tile row, of a compressed column
     __shared__ __attribute__((aligned(16))) uint8_t q8[128 * kLd];
-    __shared__ __attribute__((aligned(16))) uint8_t out[128 * kOut];
-    __shared__ __attribute__((aligned(16))) uint16_t out_meta[128 * 8];
+    uint8_t* out = q8;  // the compressed columns and their metadata, once all have been taken
+    uint16_t* out_meta = reinterpret_cast<uint16_t*>(q8 + 128 * kOut);
+    static_assert(128 * (kOut + 16) <= (int)sizeof(q8), "columns fit the tile's place");
     __shared__ uint32_t bits[128][5];  // mask words of the tile's rows (padded against bank conflicts)
     __shared__ uint32_t wmax[4], table[16];
     const int64_t cblocks = (cols + 127) / 128, rblocks = (rows + 127) / 128;
@@ -284,6 +287,7 @@ __global__ __launch_bounds__(256) void compress24_fp8_kernel(
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j][g2 >> 1] = take_two(entry[0][j], col[0][j], entry[1][j], col[1][j]);
     }
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         *reinterpret_cast<u32x2*>(&out[(4 * cq + j) * kOut + 8 * part]) = u32x2{v[j][0], v[j][1]};

@@ -211,7 +211,7 @@ def _weight(rng, m, k, dtype="bf16"):
     return w, wv, keep
 
 
-SHAPES = [(4, 4), (16, 128), (100, 132), (260, 516), (128, 1024), (512, 256)]
+SHAPES = [(4, 4), (16, 128), (100, 132), (260, 516), (128, 1024), (512, 256), (96, 60)]
 
 
 @pytest.mark.parametrize("m,k", SHAPES)
@@ -458,11 +458,12 @@ def test_gemm_tiles_exact(p, q, k):
     assert bool((buf == 7.0).all())
 
 
-def test_gemm_no_tokens_gives_zeros():
+@pytest.mark.parametrize("p,q", [(24, 40), (300, 520), (4100, 4104)])
+def test_gemm_no_tokens_gives_zeros(p, q):
     import torch
-    x = torch.empty((0, 40), dtype=torch.bfloat16, device="cuda")
-    g = torch.empty((0, 24), dtype=torch.bfloat16, device="cuda")
-    out = torch.full((24, 40), 5.0, device="cuda")
+    x = torch.empty((0, q), dtype=torch.bfloat16, device="cuda")
+    g = torch.empty((0, p), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((p, q), 5.0, device="cuda")
     sms.gemm_fp8(sms.quant_fp8(g, transpose=True), sms.quant_fp8(x, transpose=True), out=out)
     sync()
     assert bool((out == 0).all())
