@@ -29,7 +29,9 @@
  * asynchronous on `stream`, argument errors found on the host before any HIP
  * call.  No entry point allocates, keeps or shares any memory between calls,
  * records an event, or waits: calls may overlap on several streams and may be
- * captured into graphs.  Outputs must not overlap inputs.  Results are
+ * captured into graphs.  Outputs must not overlap inputs.  An operand of more
+ * than 2^40 entries, or more threads than one launch counts (2^32; 2^35 entries
+ * of X in tsenor_quant_fp8 along the rows), is _SHAPE.  Results are
  * deterministic.  A NaN in one row of X touches that row of the result only.
  */
 #ifndef TSENOR_FP8_H

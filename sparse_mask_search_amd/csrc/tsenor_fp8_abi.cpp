@@ -17,12 +17,15 @@ bool misaligned(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
 int64_t blocks128(int64_t v) { return (v + 127) / 128; }
-// rows x cols entries, without overflow
-bool too_big(int64_t rows, int64_t cols) { return cols > 0 && rows > kMaxEntries / cols; }
+// rows x cols entries, each padded by up to `pad`, without overflow
+bool too_big(int64_t rows, int64_t cols, int64_t pad = 0) {
+    return rows > kMaxEntries || cols > kMaxEntries || (cols > 0 && rows + pad > kMaxEntries / (cols + pad));
+}
 bool float_type(int t) { return t == TSENOR_F32 || t == TSENOR_BF16; }
 uintptr_t element_size(int t) { return t == TSENOR_F32 ? 4 : 2; }
 
 int status(int e, const char* where) {
+    if (e == tsenor::kGridTooLarge) return TSENOR_ERR_SHAPE;
     return e == hipSuccess ? TSENOR_OK : tsenor::hip_error(e, where);
 }
 
@@ -37,7 +40,7 @@ int tsenor_quant_fp8(const void* X, int dtype, int64_t rows, int64_t cols, int64
         (values == nullptr && values_t == nullptr) || (X == nullptr && rows != 0))
         return TSENOR_ERR_NULL;
     if (!float_type(dtype)) return TSENOR_ERR_DTYPE;
-    if (rows < 0 || cols <= 0 || ldx < cols || too_big(rows + 128, ldx + 128)) return TSENOR_ERR_SHAPE;
+    if (rows < 0 || cols <= 0 || ldx < cols || too_big(rows, ldx, 128)) return TSENOR_ERR_SHAPE;
     if (misaligned(values, 16) || misaligned(values_t, 16) || misaligned(X, element_size(dtype)))
         return TSENOR_ERR_SHAPE;
     if (rows == 0) return TSENOR_OK;
@@ -80,7 +83,7 @@ int tsenor_spmm24_fp8(const void* X, int xtype, const uint8_t* xscales, int64_t 
         (n != 0 && (X == nullptr || Y == nullptr || (xtype == TSENOR_E4M3 && xscales == nullptr))))
         return TSENOR_ERR_NULL;
     if ((xtype != TSENOR_E4M3 && xtype != TSENOR_BF16) || !float_type(ytype)) return TSENOR_ERR_DTYPE;
-    if (n < 0 || m <= 0 || k <= 0 || ldy < m || too_big(m, k + 128) || too_big(n, ldx) || too_big(n, ldy))
+    if (n < 0 || m <= 0 || k <= 0 || ldy < m || too_big(m, k, 128) || too_big(n, ldx) || too_big(n, ldy))
         return TSENOR_ERR_SHAPE;
     if (xtype == TSENOR_E4M3 ? (ldx < 128 * blocks128(k) || ldx % 16 != 0 || misaligned(X, 16))
                              : (n > 16 || ldx < k || misaligned(X, 2)))
@@ -100,7 +103,7 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
     if (C == nullptr || (k != 0 && (A == nullptr || a_scales == nullptr || B == nullptr || b_scales == nullptr)))
         return TSENOR_ERR_NULL;
     if (!float_type(ctype)) return TSENOR_ERR_DTYPE;
-    if (p <= 0 || q <= 0 || k < 0 || ldc < q || too_big(p, k + 128) || too_big(q, k + 128) || too_big(p, ldc))
+    if (p <= 0 || q <= 0 || k < 0 || ldc < q || too_big(p, k, 128) || too_big(q, k, 128) || too_big(p, ldc))
         return TSENOR_ERR_SHAPE;
     if (misaligned(A, 16) || misaligned(B, 16) || misaligned(mask, 4) || misaligned(C, element_size(ctype)))
         return TSENOR_ERR_SHAPE;

@@ -778,9 +778,12 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
          hipStream_t stream) {
     TY* Y = static_cast<TY*>(Yv);
     const bool yvec = row4<TY>(Yv, ldy);
+    bool fits = true;
     const bool tiled = !bf16x && n > 64 && m >= 64 && ldx < kMaxRow && k < kMaxRow;
     if (tiled) {
         const auto go = [&](auto kernel, int tm, int tn, int waves) {
+            fits = grid_fits(tiles(m, n, tm, tn), 64 * waves);
+            if (!fits) return;
             hipLaunchKernelGGL(kernel, dim3((unsigned)tiles(m, n, tm, tn)), dim3(64 * waves), 0, stream,
                                static_cast<const uint8_t*>(X), xs, n, ldx, values, meta, scales, m, k, Y, ldy, yvec);
         };
@@ -790,11 +793,13 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
             case 2: go(spmm24_fp8_tile_kernel<128, 64, 2, 2, 3, TY>, 128, 64, 4); break;
             default: go(spmm24_fp8_tile_kernel<64, 64, 2, 2, 3, TY>, 64, 64, 4); break;
         }
-        return (int)hipGetLastError();
+        return fits ? (int)hipGetLastError() : kGridTooLarge;
     }
     const bool xvec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && ldx % 8 == 0;
     const auto few = [&](auto kernel, int nt, int mt) {
         const int64_t ny = (n + 16 * nt - 1) / (16 * nt), nx = (m + 16 * mt - 1) / (16 * mt);
+        fits = grid_fits(nx * ny, 64 * kFewWaves);
+        if (!fits) return;
         hipLaunchKernelGGL(kernel, dim3((unsigned)(nx * ny)), dim3(64 * kFewWaves), 0, stream, X, xs, n,
                            ldx, xvec, values, meta, scales, m, k, Y, ldy, yvec);
     };
@@ -819,14 +824,17 @@ int spmm(const void* X, int bf16x, const uint8_t* xs, int64_t n, int64_t ldx, co
         else FEW(4);
 #undef FEW
     }
-    return (int)hipGetLastError();
+    return fits ? (int)hipGetLastError() : kGridTooLarge;
 }
 
 template <class TC>
 int gemm(const uint8_t* A, const uint8_t* as, int64_t p, const uint8_t* B, const uint8_t* bs,
          int64_t q, int64_t k, const uint32_t* mask, void* C, int64_t ldc, hipStream_t stream) {
+    bool fits = true;
     if (p >= 64 && q >= 64 && k < kMaxRow) {
         const auto go = [&](auto kernel, int tm, int tn, int waves) {
+            fits = grid_fits(tiles(q, p, tm, tn), 64 * waves);
+            if (!fits) return;
             hipLaunchKernelGGL(kernel, dim3((unsigned)tiles(q, p, tm, tn)), dim3(64 * waves), 0, stream, A, as, p, B,
                                bs, q, (k + 127) / 128, mask, static_cast<TC*>(C), ldc, row4<TC>(C, ldc));
         };
@@ -836,9 +844,10 @@ int gemm(const uint8_t* A, const uint8_t* as, int64_t p, const uint8_t* B, const
             case 2: go(gemm_fp8_tile_kernel<128, 64, 2, 2, 3, TC>, 128, 64, 4); break;
             default: go(gemm_fp8_tile_kernel<64, 64, 2, 2, 3, TC>, 64, 64, 4); break;
         }
-        return (int)hipGetLastError();
+        return fits ? (int)hipGetLastError() : kGridTooLarge;
     }
     const int64_t blocks = ((q + 63) / 64) * ((p + 63) / 64);
+    if (!grid_fits(blocks, 256)) return kGridTooLarge;
     hipLaunchKernelGGL((gemm_fp8_kernel<TC>), dim3((unsigned)blocks), dim3(256), 0, stream, A, as, p, B,
                        bs, q, (k + 127) / 128, mask, static_cast<TC*>(C), ldc, row4<TC>(C, ldc));
     return (int)hipGetLastError();

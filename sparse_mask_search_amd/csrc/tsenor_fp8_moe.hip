@@ -455,12 +455,16 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeJob a) {
 
 int launch_moe24_fp8(const MoeJob& a, void* stream) {
     const hipStream_t s = (hipStream_t)stream;
+    const int64_t groups = a.n * a.topk < a.experts ? a.n * a.topk : a.experts;  // chosen experts at most
+    const auto tiles = [&](int64_t length, int rows) { return groups * ((length + rows - 1) / rows); };
+    const int rows_hidden = tiles(a.f, 32) >= 512 ? 32 : 16, rows_down = tiles(a.d, 64) >= 128 ? 64 : 16;
+    if (!grid_fits(tiles(a.f, rows_hidden), 64 * kWaves) || !grid_fits(tiles(a.d, rows_down), 64 * kWaves))
+        return kGridTooLarge;
     if (a.n < 4) hipLaunchKernelGGL(moe_logits_kernel<1>, dim3((unsigned)(a.experts * a.n + a.n)), dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL(moe_logits_kernel<4>, dim3((unsigned)(a.experts * ((a.n + 3) / 4) + a.n)), dim3(256), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    const int64_t groups = a.n * a.topk < a.experts ? a.n * a.topk : a.experts;  // chosen experts at most
     const auto route = a.experts <= 64 ? moe_route_kernel<1> : a.experts <= 128 ? moe_route_kernel<2> : moe_route_kernel<8>;
     hipLaunchKernelGGL(route, dim3(1), dim3(64 * kRouteWaves), 0, s, a, (int)groups);
     e = hipGetLastError();
@@ -470,15 +474,14 @@ int launch_moe24_fp8(const MoeJob& a, void* stream) {
     // slower by 0 to 20%, as their stretches end inside the four blocks whose metadata one load
     // brings) with 16 / 32 / 64 rows: hidden, one token, 6 experts, 2048 x 1408: 9.9 / 11.6 / 12.7;
     // 33 tokens, 16 experts, 4096 x 2048: 44 / 39 / 41; down: 6.8 / 6.0 / 5.8 and 49 / 32 / 25.
-    const auto tiles = [&](int64_t length, int rows) { return groups * ((length + rows - 1) / rows); };
     const dim3 threads(64 * kWaves);
-    if (tiles(a.f, 32) >= 512)
+    if (rows_hidden == 32)
         hipLaunchKernelGGL(moe_hidden_kernel<2>, dim3((unsigned)tiles(a.f, 32)), threads, 0, s, a);
     else
         hipLaunchKernelGGL(moe_hidden_kernel<1>, dim3((unsigned)tiles(a.f, 16)), threads, 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
-    if (tiles(a.d, 64) >= 128)
+    if (rows_down == 64)
         hipLaunchKernelGGL(moe_down_kernel<4>, dim3((unsigned)tiles(a.d, 64)), threads, 0, s, a);
     else
         hipLaunchKernelGGL(moe_down_kernel<1>, dim3((unsigned)tiles(a.d, 16)), threads, 0, s, a);

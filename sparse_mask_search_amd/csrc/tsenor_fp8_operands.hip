@@ -318,6 +318,7 @@ int quant(const void* Xv, int64_t rows, int64_t cols, int64_t ldx, uint8_t* valu
     const T* X = static_cast<const T*>(Xv);
     const bool vec = rows16<T>(X, ldx);
     const int64_t cb = (cols + 127) / 128, rb = (rows + 127) / 128;
+    if (!grid_fits(values_t == nullptr ? (rows * cb + 15) / 16 : rb * cb, 256)) return kGridTooLarge;
     if (values_t == nullptr)
         hipLaunchKernelGGL((quant_rows_kernel<T>), dim3((unsigned)((rows * cb + 15) / 16)), dim3(256),
                            0, stream, X, rows, cols, ldx, vec, values, scales);
@@ -346,6 +347,7 @@ int launch_compress24_fp8(const void* W, int bf16, int64_t batch, int64_t stride
     const bool vec = (reinterpret_cast<uintptr_t>(W) & 15u) == 0 && (ld * es) % 16 == 0 &&
                      (batch == 1 || (stride * es) % 16 == 0);
     const int64_t blocks = batch * ((rows + 127) / 128) * ((cols + 127) / 128);
+    if (!grid_fits(blocks, 256)) return kGridTooLarge;
     if (bf16)
         hipLaunchKernelGGL((compress24_fp8_kernel<uint16_t>), dim3((unsigned)blocks), dim3(256), 0,
                            (hipStream_t)stream, static_cast<const uint16_t*>(W), stride, rows, cols, ld,

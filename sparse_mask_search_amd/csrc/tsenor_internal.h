@@ -73,6 +73,11 @@ int launch_compress24(const uint16_t* W, int64_t ld, const uint32_t* mask, int64
 int launch_spmm24(const uint16_t* X, int64_t ldx, const uint16_t* vals, const uint32_t* meta,
                   float* Y, int64_t ldy, int64_t n, int64_t m, int64_t k, void* stream);
 
+// A launch counts its threads in 32 bits.  Before they would pass that, the 8-bit operators'
+// launch functions return kGridTooLarge in place of a HIP error.
+constexpr int kGridTooLarge = -1;
+inline bool grid_fits(int64_t groups, int threads) { return groups <= (int64_t)0xFFFFFFFF / threads; }
+
 // Builders of the 8-bit operands (tsenor_fp8_operands.hip).
 int launch_quant_fp8(const void* X, int bf16, int64_t rows, int64_t cols, int64_t ldx,
                      uint8_t* values, uint8_t* scales, uint8_t* values_t, uint8_t* scales_t,

@@ -114,6 +114,33 @@ def test_moe_rejects(kw, code):
     assert moe(**kw) == code
 
 
+HUGE = (1 << 63) - 1
+
+
+@pytest.mark.parametrize("call,kw", [
+    (quant, dict(rows=HUGE)), (quant, dict(cols=HUGE, ld=HUGE)), (quant, dict(ld=HUGE)), (quant, dict(rows=HUGE, cols=1)),
+    (compress, dict(batch=HUGE)), (compress, dict(rows=HUGE - 3)), (compress, dict(cols=HUGE - 3, ld=HUGE)),
+    (compress, dict(stride=HUGE)), (spmm, dict(n=HUGE)), (spmm, dict(m=HUGE, ldy=HUGE)), (spmm, dict(k=HUGE)),
+    (spmm, dict(ldy=HUGE)), (spmm, dict(k=HUGE, ldx=HUGE - 15)), (gemm, dict(p=HUGE)), (gemm, dict(q=HUGE, ldc=HUGE)),
+    (gemm, dict(k=HUGE)), (gemm, dict(ldc=HUGE)), (moe, dict(d=HUGE, ldx=HUGE, ldr=HUGE, ldy=HUGE)), (moe, dict(f=HUGE)),
+    (moe, dict(ldx=HUGE)), (moe, dict(ldr=HUGE)), (moe, dict(ldy=HUGE)),
+])
+def test_sums_of_sizes_do_not_wrap(call, kw):
+    assert call(**kw) == SHAPE
+
+
+@pytest.mark.parametrize("call,kw", [
+    (quant, dict(rows=1 << 28, cols=129, ld=129, vt=None, st=None)),     # 2^25 workgroups of 256 threads
+    (quant, dict(rows=1 << 31, cols=129, ld=129)),                       # 2^25 tiles
+    (compress, dict(batch=1 << 24, stride=4096)),
+    (spmm, dict(n=1, m=1 << 28, k=64, ldy=1 << 28)),                     # 2^24 workgroups of 512 threads
+    (gemm, dict(p=1 << 31, q=40, k=1)),
+    (moe, dict(n=64, e=512, topk=8, f=1 << 20, size=1 << 40)),           # 2^24 workgroups of 256 threads
+])
+def test_grids_past_a_launch_are_refused(call, kw):
+    assert call(**kw) == SHAPE
+
+
 def test_moe_workspace():
     w = sms.lib().tsenor_moe24_fp8_workspace
     assert w(4, 64, 32, 8, 2) >= 4 * 8 * 8 + 4 * 128 * 2 + 8 * 128 * 2 + 8 * 4
