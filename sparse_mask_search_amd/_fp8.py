@@ -125,8 +125,25 @@ def _sparse(torch, a, device, name, lead, rows=None):
     return rows
 
 
-def _out(torch, out, shape, dtype, near):
-    """A fresh result on the device of `near`, or `out` after checking it."""
+def _apart(out, x):
+    """Refuses an `out` that shares bytes with the input x (both [rows, cols])."""
+    def span(t):
+        width = t.shape[1] * t.element_size()
+        pitch = _ld(t) * t.element_size()
+        return t.data_ptr(), width, pitch, (t.shape[0] - 1) * pitch + width
+    if out.numel() == 0 or x.numel() == 0:
+        return
+    (a, aw, ap, an), (b, bw, bp, bn) = span(out), span(x)
+    if a + an <= b or b + bn <= a:
+        return
+    if ap == bp and aw <= (b - a) % ap <= ap - bw:  # columns of one buffer, side by side
+        return
+    raise ValueError("out overlaps the input")
+
+
+def _out(torch, out, shape, dtype, near, x=None):
+    """A fresh result on the device of `near`, or `out` after checking it (and that it does not
+    overlap the tensor x)."""
     if out is None:
         return near.new_empty(shape, dtype=dtype or torch.bfloat16)
     device = near.device
@@ -136,6 +153,8 @@ def _out(torch, out, shape, dtype, near):
                          + (f" and type {dtype}" if dtype is not None else ""))
     if shape[0] > 1 and out.stride(0) < shape[1]:
         raise ValueError("the rows of out overlap")
+    if x is not None:
+        _apart(out, x)
     return out
 
 
@@ -222,7 +241,7 @@ def spmm24_fp8(torch, X, A, out=None, dtype=None):
     """Y = X A^T with A a Sparse24Fp8 operand [m, k] (tsenor_spmm24_fp8).  X: a
     DenseFp8 operand [n, k], or a bf16 or f32 tensor, which is quantised along
     its rows first.  Returns [n, m] in `dtype` (bf16 unless given or taken from
-    `out`)."""
+    `out`, which must not overlap X)."""
     ready = isinstance(X, DenseFp8)
     if ready:
         device = X.values.device
@@ -234,7 +253,7 @@ def spmm24_fp8(torch, X, A, out=None, dtype=None):
     m = _sparse(torch, A, device, "A", ())
     if A.k != k:
         raise ValueError(f"X has {k} columns, A has {A.k}")
-    out = _out(torch, out, (n, m), dtype, A.values)
+    out = _out(torch, out, (n, m), dtype, A.values, None if ready else X)
     yt = _float_type(torch, out, "out")
     if n == 0 or m == 0:
         return out
@@ -290,7 +309,7 @@ def moe24_fp8(torch, x, router, gate, up, down, topk: int, out=None, return_rout
     _sparse(torch, down, device, "down", (experts,), d)
     if gate.k != d or up.k != d or down.k != f:
         raise ValueError(f"gate and up must have {d} columns, down {f}")
-    out = _out(torch, out, (n, d), torch.bfloat16, x)
+    out = _out(torch, out, (n, d), torch.bfloat16, x, x)
     ids = torch.empty((n, topk), dtype=torch.int32, device=device) if return_routing else None
     weights = torch.empty((n, topk), dtype=torch.float32, device=device) if return_routing else None
     size = lib().tsenor_moe24_fp8_workspace(n, d, f, experts, topk)

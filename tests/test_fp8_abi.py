@@ -169,3 +169,39 @@ def test_reference_rounding():
     assert ref.round_e4m3(np.array([17.0, 19.0, 2.0 ** -10, 3 * 2.0 ** -10])).tolist() == [
         ref.round_e4m3(np.array([16.0]))[0], ref.round_e4m3(np.array([20.0]))[0], 0, 2]
     assert ref.exponent(np.array([448.0, 448.0001, 0.0, 1e-45, 3.3e38])).tolist() == [0, 1, 0, -127, 120]
+
+
+@pytest.mark.parametrize("x,out,fine", [
+    (np.s_[0:4, 0:32], np.s_[0:4, 32:64], True),     # side by side in one buffer
+    (np.s_[0:4, 32:64], np.s_[0:4, 0:32], True),
+    (np.s_[0:4, :], np.s_[4:8, :], True),            # one above the other
+    (np.s_[2:3, 0:8], np.s_[0:8, 8:64], True),       # one row beside many
+    (np.s_[0:4, 0:32], np.s_[0:4, 0:32], False),
+    (np.s_[0:4, 0:33], np.s_[0:4, 32:64], False),
+    (np.s_[0:4, 31:64], np.s_[0:4, 0:32], False),
+    (np.s_[0:4, :], np.s_[3:7, :], False),
+    (np.s_[2:3, 0:9], np.s_[0:8, 8:64], False),
+    (np.s_[0:0, :], np.s_[0:0, :], True),
+])
+def test_outputs_over_inputs_are_found(x, out, fine):
+    import torch
+    from sparse_mask_search_amd import _fp8
+    buf = torch.zeros((8, 64), dtype=torch.bfloat16)
+    if fine:
+        _fp8._apart(buf[out], buf[x])
+    else:
+        with pytest.raises(ValueError, match="overlaps"):
+            _fp8._apart(buf[out], buf[x])
+    _fp8._apart(torch.zeros((8, 64)), buf)
+
+
+def test_outputs_over_inputs_of_another_width():
+    import torch
+    from sparse_mask_search_amd import _fp8
+    buf = torch.zeros((4, 64), dtype=torch.float32)
+    halves = buf.view(torch.bfloat16)  # the same rows, 128 entries each
+    _fp8._apart(buf[:, 32:], halves[:, :64])
+    with pytest.raises(ValueError, match="overlaps"):
+        _fp8._apart(buf[:, 31:], halves[:, :64])
+    with pytest.raises(ValueError, match="overlaps"):
+        _fp8._apart(buf.view(8, 32), halves[:, :64])  # other rows over the same bytes

@@ -756,3 +756,19 @@ def test_refusals_on_tensors():
         sms.moe24_fp8(torch.zeros((65, 128), dtype=torch.bfloat16, device="cuda"), r, st(A), st(A), st(down), 1)
     with pytest.raises(ValueError):
         sms.moe24_fp8(x, r, st(A), st(down), st(down), 1)
+
+
+@pytest.mark.parametrize("n", [3, 16, 20, 70])
+def test_spmm_out_beside_or_over_its_input(n):
+    import torch
+    rng = np.random.default_rng(n)
+    w, _, keep = _weight(rng, 64, 64)
+    A, _ = sms.compress24_fp8(w, words(keep))
+    buf = torch.from_numpy(rng.standard_normal((n, 128)).astype(np.float32)).to(torch.bfloat16).cuda()
+    want = sms.spmm24_fp8(buf[:, :64].clone(), A)
+    with pytest.raises(ValueError):
+        sms.spmm24_fp8(buf[:, :64], A, out=buf[:, :64])
+    with pytest.raises(ValueError):
+        sms.spmm24_fp8(buf[:, :64], A, out=buf[:, 32:96])
+    sms.spmm24_fp8(buf[:, :64], A, out=buf[:, 64:])
+    assert torch.equal(buf[:, 64:], want)
