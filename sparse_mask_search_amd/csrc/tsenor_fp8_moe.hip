@@ -49,9 +49,9 @@ __device__ __forceinline__ int place_of(int k) {
     return (k & ~127) | (8 * (4 * (2 * j + half) + q)) | (k & 7);
 }
 
-// logits[e][t] in fp64 (products of bf16 numbers are exact in fp32).  A workgroup
-// per expert and kLogitTokens tokens, its four waves a quarter of d each; the workgroups
-// behind those copy x.
+// logits[e][t] in fp64, products too (those of bf16 numbers reach from 2^-266 to 2^256: fp32
+// loses the ends).  A workgroup per expert and kLogitTokens tokens, its four waves a quarter of
+// d each; the workgroups behind those copy x.
 template <int kLogitTokens>
 __global__ __launch_bounds__(256) void moe_logits_kernel(MoeJob a) {
     __shared__ double part[4][kLogitTokens];
@@ -75,9 +75,11 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(MoeJob a) {
 #pragma unroll
         for (int j = 0; j < kLogitTokens; ++j) load8(x[j], i, a.d, a.xvec, xv[j]);
 #pragma unroll
-        for (int j = 0; j < kLogitTokens; ++j)
+        for (int c = 0; c < 8; ++c) {
+            const double w = (double)widen(rv[c]);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) sum[j] += (double)(widen(xv[j][c]) * widen(rv[c]));
+            for (int j = 0; j < kLogitTokens; ++j) sum[j] = __builtin_fma((double)widen(xv[j][c]), w, sum[j]);
+        }
     }
 #pragma unroll
     for (int j = 0; j < kLogitTokens; ++j) {
