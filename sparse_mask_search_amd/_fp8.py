@@ -309,6 +309,8 @@ def moe24_fp8(torch, x, router, gate, up, down, topk: int, out=None, return_rout
     _sparse(torch, down, device, "down", (experts,), d)
     if gate.k != d or up.k != d or down.k != f:
         raise ValueError(f"gate and up must have {d} columns, down {f}")
+    if not 1 <= topk <= experts:  # the library would see its low 32 bits
+        raise TsenorError(4, "tsenor_moe24_fp8")  # TSENOR_ERR_PARAM
     out = _out(torch, out, (n, d), torch.bfloat16, x, x)
     ids = torch.empty((n, topk), dtype=torch.int32, device=device) if return_routing else None
     weights = torch.empty((n, topk), dtype=torch.float32, device=device) if return_routing else None

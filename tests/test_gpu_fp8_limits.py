@@ -25,3 +25,16 @@ def test_moe_router_products_outside_fp32(n):
     sync()
     assert ids.tolist() == [[1, 3, 0, 2]] * n
     assert wts.tolist() == [[1.0, 0.0, 0.0, 0.0]] * n
+
+
+def test_moe_topk_past_32_bits_is_refused():
+    """The library takes an int: 2^32 + 1 must not arrive there as 1."""
+    import torch
+    rng = np.random.default_rng(1)
+    gate, up, down = _experts(rng, 2, 64, 64)[0], _experts(rng, 2, 64, 64)[0], _experts(rng, 2, 64, 64)[0]
+    x, r = torch.zeros((1, 64), dtype=torch.bfloat16).cuda(), torch.zeros((2, 64), dtype=torch.bfloat16).cuda()
+    for topk in (2 ** 32 + 1, -2 ** 32 + 1, 2 ** 31, -1, 0, 3):
+        for routing in (False, True):
+            with pytest.raises(sms.TsenorError):
+                sms.moe24_fp8(x, r, gate, up, down, topk, return_routing=routing)
+    assert sms.moe24_fp8(x, r, gate, up, down, 1).shape == (1, 64)
