@@ -11,6 +11,7 @@ tensors' device.
 from __future__ import annotations
 
 import functools
+import inspect
 from typing import NamedTuple
 
 from . import _lib
@@ -44,23 +45,34 @@ def _blocks(k: int) -> int:
 
 
 def _placed(fn):
-    """Run fn on its first argument's device, and on `stream` if one is given."""
+    """fn without its leading torch argument: run on its first argument's device, and on
+    `stream` if one is given."""
+    signature = inspect.signature(fn)
+    params = list(signature.parameters.values())[1:]
+    first = params[0].name
+
     @functools.wraps(fn)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         torch = _lib._torch()
+        if not args and first not in kw:
+            raise TypeError(f"{fn.__name__}() missing required argument: '{first}'")
+        x = args[0] if args else kw[first]
         t = x.values if isinstance(x, (DenseFp8, Sparse24Fp8)) else x
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{fn.__name__} needs CUDA (HIP) torch tensors")
         device = t.device
         if stream is None and device.index == torch.cuda.current_device():
-            return fn(torch, x, *args, **kw)
+            return fn(torch, *args, **kw)
         if stream is None:
             with torch.cuda.device(device):
-                return fn(torch, x, *args, **kw)
+                return fn(torch, *args, **kw)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
-            return fn(torch, x, *args, **kw)
+            return fn(torch, *args, **kw)
+
+    call.__signature__ = signature.replace(
+        parameters=params + [inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 
