@@ -137,25 +137,33 @@ def _sparse(torch, a, device, name, lead, rows=None):
     return rows
 
 
-def _apart(out, x):
-    """Refuses an `out` that shares bytes with the input x (both [rows, cols])."""
-    def span(t):
-        width = t.shape[1] * t.element_size()
-        pitch = _ld(t) * t.element_size()
+def _span(t):
+    """First byte, bytes of a row, bytes from row to row, bytes in all (a contiguous tensor of
+    another dimension counts as one row)."""
+    if t.dim() == 2:
+        width, pitch = t.shape[1] * t.element_size(), _ld(t) * t.element_size()
         return t.data_ptr(), width, pitch, (t.shape[0] - 1) * pitch + width
+    size = t.numel() * t.element_size()
+    return t.data_ptr(), size, size, size
+
+
+def _apart(out, x):
+    """Refuses an `out` that shares bytes with the input x."""
     if out.numel() == 0 or x.numel() == 0:
         return
-    (a, aw, ap, an), (b, bw, bp, bn) = span(out), span(x)
+    (a, aw, ap, an), (b, bw, bp, bn) = _span(out), _span(x)
     if a + an <= b or b + bn <= a:
         return
     if ap == bp and aw <= (b - a) % ap <= ap - bw:  # columns of one buffer, side by side
         return
-    raise ValueError("out overlaps the input")
+    if aw <= (b - a) % ap <= ap - bn or bw <= (a - b) % bp <= bp - an:  # one whole between two rows
+        return
+    raise ValueError("out overlaps an input")
 
 
-def _out(torch, out, shape, dtype, near, x=None):
+def _out(torch, out, shape, dtype, near, inputs):
     """A fresh result on the device of `near`, or `out` after checking it (and that it does not
-    overlap the tensor x)."""
+    overlap any of the tensors `inputs`; an operand stands for its parts)."""
     if out is None:
         return near.new_empty(shape, dtype=dtype or torch.bfloat16)
     device = near.device
@@ -165,8 +173,10 @@ def _out(torch, out, shape, dtype, near, x=None):
                          + (f" and type {dtype}" if dtype is not None else ""))
     if shape[0] > 1 and out.stride(0) < shape[1]:
         raise ValueError("the rows of out overlap")
-    if x is not None:
-        _apart(out, x)
+    for x in inputs:
+        for part in x[:-1] if isinstance(x, (DenseFp8, Sparse24Fp8)) else (x,):
+            if part is not None:
+                _apart(out, part)
     return out
 
 
@@ -253,7 +263,7 @@ def spmm24_fp8(torch, X, A, out=None, dtype=None):
     """Y = X A^T with A a Sparse24Fp8 operand [m, k] (tsenor_spmm24_fp8).  X: a
     DenseFp8 operand [n, k], or a bf16 or f32 tensor, which is quantised along
     its rows first.  Returns [n, m] in `dtype` (bf16 unless given or taken from
-    `out`, which must not overlap X)."""
+    `out`, which must not overlap X or A)."""
     ready = isinstance(X, DenseFp8)
     if ready:
         device = X.values.device
@@ -265,7 +275,7 @@ def spmm24_fp8(torch, X, A, out=None, dtype=None):
     m = _sparse(torch, A, device, "A", ())
     if A.k != k:
         raise ValueError(f"X has {k} columns, A has {A.k}")
-    out = _out(torch, out, (n, m), dtype, A.values, None if ready else X)
+    out = _out(torch, out, (n, m), dtype, A.values, (X, A))
     yt = _float_type(torch, out, "out")
     if n == 0 or m == 0:
         return out
@@ -284,7 +294,9 @@ def gemm_fp8(torch, A, B, mask=None, out=None, dtype=None):
     """C = A B^T for DenseFp8 operands A [p, k] and B [q, k]; with a mask (int32
     words [p, ceil(q / 32)]) the removed entries are 0 (tsenor_gemm_fp8).  The
     masked weight gradient of Y = X W^T is
-    gemm_fp8(quant_fp8(dY, transpose=True), quant_fp8(X, transpose=True), mask)."""
+    gemm_fp8(quant_fp8(dY, transpose=True), quant_fp8(X, transpose=True), mask).
+    Returns [p, q] in `dtype` (bf16 unless given or taken from `out`, which must
+    not overlap A, B or the mask)."""
     if not isinstance(A, DenseFp8):
         raise TypeError("A must be a DenseFp8 operand (quant_fp8)")
     device = A.values.device
@@ -293,7 +305,7 @@ def gemm_fp8(torch, A, B, mask=None, out=None, dtype=None):
         raise ValueError(f"A has {A.k} columns, B has {B.k}")
     if mask is not None:
         _part(torch, mask, torch.int32, (p, (q + 31) // 32), device, "mask")
-    out = _out(torch, out, (p, q), dtype, A.values)
+    out = _out(torch, out, (p, q), dtype, A.values, (A, B, mask))
     ct = _float_type(torch, out, "out")
     if p == 0 or q == 0:
         return out
@@ -307,8 +319,9 @@ def gemm_fp8(torch, A, B, mask=None, out=None, dtype=None):
 def moe24_fp8(torch, x, router, gate, up, down, topk: int, out=None, return_routing: bool = False):
     """A mixture-of-experts layer for up to 64 tokens (tsenor_moe24_fp8): x bf16
     [n, d], router bf16 [experts, d], gate and up stacks of Sparse24Fp8 operands
-    [experts, f, d], down [experts, d, f].  Returns y bf16 [n, d], or with
-    return_routing (y, ids int32 [n, topk], weights fp32 [n, topk])."""
+    [experts, f, d], down [experts, d, f].  Returns y bf16 [n, d] (`out`, which
+    must not overlap any of them), or with return_routing (y, ids int32 [n, topk],
+    weights fp32 [n, topk])."""
     _matrix(torch, x, "x")
     _matrix(torch, router, "router")
     if x.dtype != torch.bfloat16 or router.dtype != torch.bfloat16:
@@ -323,7 +336,7 @@ def moe24_fp8(torch, x, router, gate, up, down, topk: int, out=None, return_rout
         raise ValueError(f"gate and up must have {d} columns, down {f}")
     if not 1 <= topk <= experts:  # the library would see its low 32 bits
         raise TsenorError(4, "tsenor_moe24_fp8")  # TSENOR_ERR_PARAM
-    out = _out(torch, out, (n, d), torch.bfloat16, x, x)
+    out = _out(torch, out, (n, d), torch.bfloat16, x, (x, router, gate, up, down))
     ids = torch.empty((n, topk), dtype=torch.int32, device=device) if return_routing else None
     weights = torch.empty((n, topk), dtype=torch.float32, device=device) if return_routing else None
     size = lib().tsenor_moe24_fp8_workspace(n, d, f, experts, topk)

@@ -30,3 +30,30 @@ def test_arguments_have_names(name):
         fn(**{p.name: torch.zeros(8, 128) for p in needed})
     with pytest.raises(TypeError, match=needed[0].name):
         fn()
+
+
+def _refused(out, x):
+    from sparse_mask_search_amd import _fp8
+    try:
+        _fp8._apart(out, x)
+    except ValueError:
+        return True
+    return False
+
+
+def test_outputs_over_operands_are_found():
+    """Parts of operands are contiguous, of two dimensions or (stacked) three: they may lie before,
+    behind or whole between two rows of a strided output."""
+    buf = torch.zeros((6, 64), dtype=torch.bfloat16)
+    flat = buf.view(-1)
+    out = buf[1:5, :16]
+    for first, size, over in ((0, 64, False), (0, 65, True), (64, 8, True), (80, 48, False), (79, 8, True),
+                              (80, 49, True), (208, 48, False), (272, 64, False), (271, 8, True), (100, 100, True)):
+        part = flat[first:first + size]
+        assert _refused(out, part.view(1, size)) == over, (first, size)
+        assert _refused(out, part.view(1, 1, size)) == over, (first, size)
+        assert _refused(part.view(1, size), out) == over, (first, size)
+    # several rows of an operand between two rows of the output, and over one
+    assert not _refused(out, flat[144:176].view(4, 8))
+    assert _refused(out, flat[144:200].view(7, 8))
+    assert not _refused(out, flat[:0].view(1, 0))

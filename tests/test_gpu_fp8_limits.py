@@ -2,8 +2,9 @@
 import numpy as np
 import pytest
 
+import fp8_ref as ref
 import sparse_mask_search_amd as sms
-from test_gpu_fp8 import _experts, say, sync
+from test_gpu_fp8 import _experts, say, sync, tensor, words
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,44 @@ def test_moe_topk_past_32_bits_is_refused():
             with pytest.raises(sms.TsenorError):
                 sms.moe24_fp8(x, r, gate, up, down, topk, return_routing=routing)
     assert sms.moe24_fp8(x, r, gate, up, down, 1).shape == (1, 64)
+
+
+# ---- results over operands -----------------------------------------------------------
+
+def test_out_over_any_operand_is_refused():
+    """The products read their operands while others of their workgroups write already."""
+    import torch
+    rng = np.random.default_rng(2)
+    n = m = 64
+    w, _ = tensor(rng.standard_normal((m, 256)), "bf16")
+    A, _ = sms.compress24_fp8(w, words(ref.random24(rng, m, 256)))
+    x, _ = tensor(rng.standard_normal((n, 256)), "bf16")
+    X, B = sms.quant_fp8(x), sms.quant_fp8(w)
+    mask = torch.full((n, 2), -1, dtype=torch.int32, device="cuda")
+    over = lambda t, cols=64: t.view(torch.bfloat16)[:, :cols]
+    for out in (over(X.values), over(A.values)):
+        with pytest.raises(ValueError, match="overlaps"):
+            sms.spmm24_fp8(X, A, out=out)
+    with pytest.raises(ValueError, match="overlaps"):
+        sms.spmm24_fp8(x, A, out=over(A.values))
+    for out in (over(X.values), over(B.values)):
+        with pytest.raises(ValueError, match="overlaps"):
+            sms.gemm_fp8(X, B, out=out)
+    words4 = torch.full((n, 64), -1, dtype=torch.int32, device="cuda").view(-1)[:n * 2].view(n, 2)
+    with pytest.raises(ValueError, match="overlaps"):
+        sms.gemm_fp8(X, B, mask=words4, out=torch.as_strided(words4, (n, 64), (64, 1)).view(torch.float32))
+    gate, up, down = (_experts(rng, n, 64, 64)[0] for _ in range(3))
+    r, _ = tensor(rng.standard_normal((n, 64)), "bf16")
+    t = x[:, :64].contiguous()
+    for out in (r, t, gate.values.view(torch.bfloat16).view(n, -1)[:, :64], down.meta.view(torch.bfloat16).view(n, -1)[:, :64]):
+        with pytest.raises(ValueError, match="overlaps"):
+            sms.moe24_fp8(t, r, gate, up, down, 2, out=out)
+    # beside them it is taken, and nothing of the operand changes
+    buf = torch.zeros((n, 128), dtype=torch.bfloat16, device="cuda")
+    buf[:, 64:] = r
+    want = sms.moe24_fp8(t, r, gate, up, down, 2)
+    got = sms.moe24_fp8(t, buf[:, 64:], gate, up, down, 2, out=buf[:, :64])
+    sync()
+    assert torch.equal(got, want) and torch.equal(buf[:, 64:], r)
+    assert torch.equal(sms.gemm_fp8(X, B, mask=mask, out=torch.empty((n, m), device="cuda")),
+                       sms.gemm_fp8(X, B, dtype=torch.float32))
