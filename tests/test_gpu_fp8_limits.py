@@ -4,7 +4,7 @@ import pytest
 
 import fp8_ref as ref
 import sparse_mask_search_amd as sms
-from test_gpu_fp8 import _experts, say, sync, tensor, words
+from test_gpu_fp8 import _experts, f64, integers, say, sync, tensor, words
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,62 @@ def test_out_over_any_operand_is_refused():
     assert torch.equal(got, want) and torch.equal(buf[:, 64:], r)
     assert torch.equal(sms.gemm_fp8(X, B, mask=mask, out=torch.empty((n, m), device="cuda")),
                        sms.gemm_fp8(X, B, dtype=torch.float32))
+
+
+# ---- unused slots of a group -------------------------------------------------------
+
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_spmm_nan_at_removed_positions(n):
+    """A group with fewer than two kept entries has unused slots: zeros that point at the positions
+    0 and 1 of an empty group, at 3 beside one kept entry (2 if that is itself at 3).  A NaN
+    there reaches the result, at the other removed positions it does not."""
+    import torch
+    say("removed positions", n)
+    rng = np.random.default_rng(n)
+    m, k = 132, 260
+    keep = ref.random24(rng, m, k)
+    keep[:5] = False                       # row 4 stays empty
+    for p in range(4):
+        keep[p, p::4] = True               # row p keeps position p of each group
+    w, _ = tensor(integers(rng, (m, k), 7) + 8, "bf16")
+    A, _ = sms.compress24_fp8(w, words(keep))
+    wv = f64(w) * keep
+    xv = integers(rng, (n, k), 7)
+    reach = np.array([[1, 0, 0, 1], [0, 1, 0, 1], [0, 0, 1, 1], [0, 0, 1, 1], [1, 1, 0, 0]], bool)
+    full = np.concatenate([np.tile(reach, (1, k // 4)), keep[5:]])
+    for j in (0, 1, 2, 3, 130, 131, 256, 259):
+        x = torch.from_numpy(xv.astype(np.float32)).bfloat16().cuda()
+        x[1, j] = float("nan")
+        for X in (x, sms.quant_fp8(x)):
+            y = sms.spmm24_fp8(X, A, dtype=torch.float32)
+            sync()
+            got = f64(y)
+            assert np.array_equal(np.isnan(got[1]), full[:, j]), j
+            clean = np.ones_like(got, bool)
+            clean[1] = ~full[:, j]
+            assert np.array_equal(got[clean], (xv @ wv.T)[clean])   # small integers: exact
+
+
+@pytest.mark.parametrize("j", [40, 41, 42, 43])
+def test_moe_infinite_hidden_entry_at_removed_positions(j):
+    """Entry j of the hidden vector is infinite, the others are 0.  Row 0 of down is empty: it
+    meets the infinity (0 * inf) where its unused slots point at it, else it is 0."""
+    import torch
+    rng = np.random.default_rng(j)
+    d = f = 128
+    gate, _ = sms.compress24_fp8(torch.ones((1, f, d)).cuda(), words(ref.random24(rng, f, d))[None])
+    u = torch.zeros((1, f, d))
+    u[0, j] = 2.0 ** 120
+    up, _ = sms.compress24_fp8(u.cuda(), words(ref.random24(rng, f, d))[None])
+    keep = ref.random24(rng, d, f)
+    keep[0] = False
+    down, _ = sms.compress24_fp8(torch.ones((1, d, f)).cuda(), words(keep)[None])
+    x = torch.full((1, d), 16.0, dtype=torch.bfloat16, device="cuda")
+    y = sms.moe24_fp8(x, torch.zeros((1, d), dtype=torch.bfloat16, device="cuda"), gate, up, down, 1)
+    sync()
+    got = f64(y)[0]
+    assert np.array_equal(np.isinf(got), keep[:, j])
+    assert np.isnan(got[0]) == (j % 4 < 2)
+    rest = ~keep[:, j]
+    rest[0] = j % 4 >= 2
+    assert (got[rest] == 0).all()
