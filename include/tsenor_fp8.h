@@ -113,7 +113,8 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
  *   largest (ties to the lowest index, NaN below every number) with weights
  *   softmax over those; y = sum_e w_e Down_e (silu(Gate_e x) * (Up_e x)).  The
  *   hidden vector is held as the sum of two bf16 numbers (2^-16 of each entry
- *   at most is lost), y is rounded once.
+ *   at most is lost), y is rounded once.  Weights are multiplied as bf16 numbers:
+ *   they lose bits below 2^-133, and a magnitude of 2^128 or more is infinite.
  *   X [n][ldx] bf16, 0 <= n <= 64;  router [experts][ldr] bf16;
  *   gate, up  batches of `experts` 2:4 operands [f][d];  down  [d][f];
  *   workspace device memory of at least tsenor_moe24_fp8_workspace(...) bytes,

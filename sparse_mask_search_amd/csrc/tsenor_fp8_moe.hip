@@ -14,9 +14,10 @@
 // The hidden entries are kept as the sum of two bf16 numbers (16 fraction bits;
 // one alone would lose as much as the rounding of y itself), which costs two more
 // matrix instructions per block where the memory is waited for.
-// The weights' 8-bit numbers become bf16 exactly, their scale folded into the
-// conversion (v_cvt_scalef32_pk_bf16_fp8), and multiply the bf16 activations on
-// the sparse matrix cores (v_smfmac_f32_16x16x64_bf16).  Operand layout of that
+// The weights' 8-bit numbers become bf16, their scale folded into the conversion
+// (v_cvt_scalef32_pk_bf16_fp8): exactly, subnormal ones too, but for bits below 2^-133
+// (blocks with a scale below 2^-124).  They multiply the bf16 activations on the sparse
+// matrix cores (v_smfmac_f32_16x16x64_bf16).  Operand layout of that
 // instruction (measured with an in-bounds probe), lane l, q = l / 16: A row
 // l % 16, eight values that cover 16 entries; when these are entries
 // 32q + 16j .. 32q + 16j + 15 of a block of 128 (j = 0, 1: the two instructions
@@ -239,7 +240,7 @@ __device__ __forceinline__ void load_block(const uint16_t* x, int q, bf16x16 b[2
         b[j] = __builtin_bit_cast(bf16x16, w);
     }
 }
-// The conversion takes the exponent field of its scale operand: the byte itself.
+// The conversion takes the exponent field of its scale operand: the byte itself (0 is 2^-127).
 __device__ __forceinline__ float scale_value(int byte) { return bits_float((uint32_t)byte << 23); }
 
 // hidden: one workgroup per (chosen expert, 16 MT rows of gate and up).

@@ -4,7 +4,7 @@ import pytest
 
 import fp8_ref as ref
 import sparse_mask_search_amd as sms
-from test_gpu_fp8 import _experts, f64, integers, say, sync, tensor, words
+from test_gpu_fp8 import _experts, _moe_reference, bytes_of, close, f64, integers, say, sync, tensor, words
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,41 @@ def test_moe_infinite_hidden_entry_at_removed_positions(j):
     rest = ~keep[:, j]
     rest[0] = j % 4 >= 2
     assert (got[rest] == 0).all()
+
+
+# ---- the expert layer at the ends of the scales --------------------------------------
+
+@pytest.mark.parametrize("byte", [0, 1, 2, 9, 12, 60, 200, 245])
+@pytest.mark.parametrize("which", ["gate", "up", "down"])
+@pytest.mark.filterwarnings("ignore:overflow encountered in exp")   # silu of a large negative number
+def test_moe_scales_at_the_ends(which, byte):
+    """One operand's blocks all have the scale 2^(byte - 127).  Weights become bf16 numbers,
+    subnormal ones too, so the lowest scales lose what lies below 2^-133 of a weight (at most
+    2^-134 by rounding) and nothing else; the tokens and the other operands bring the layer back
+    into range."""
+    import torch
+    say("moe scales", which, byte)
+    rng = np.random.default_rng(byte)
+    n, d, f = 3, 256, 132
+    ops = {"gate": _experts(rng, 1, f, d)[0], "up": _experts(rng, 1, f, d)[0], "down": _experts(rng, 1, d, f)[0]}
+    shift = max(-100, min(100, 117 - byte)) if which != "down" else 0
+    for name, a in ops.items():
+        s = a.scales.view(torch.uint8)
+        s.fill_(byte if name == which else 117 if name == "down" else max(1, 117 - shift))
+    x, xv = tensor(rng.standard_normal((n, d)) * 2.0 ** shift, "bf16")
+    r = torch.zeros((1, d), dtype=torch.bfloat16, device="cuda")
+    y = sms.moe24_fp8(x, r, ops["gate"], ops["up"], ops["down"], 1)
+    sync()
+    dense = {name: ref.expand(bytes_of(a.values)[0], a.meta[0].cpu().numpy().view(np.uint32),
+                              bytes_of(a.scales)[0])[None] for name, a in ops.items()}
+    gate, up, down = dense["gate"][:, :, :d], dense["up"][:, :, :d], dense["down"][:, :, :f]
+    want, bound = _moe_reference(xv, np.zeros((n, 1), int), np.ones((n, 1)), gate, up, down)
+    g, u = xv @ gate[0].T, xv @ up[0].T
+    silu, lost = g / (1 + np.exp(-g)), 2.0 ** -134
+    reach = lost * np.abs(xv).sum(1, keepdims=True)
+    if which == "down":
+        bound = bound + lost * np.abs(silu * u).sum(1, keepdims=True)
+    else:
+        dh = 1.1 * reach * np.abs(u) if which == "gate" else reach * np.abs(silu)
+        bound = bound + dh @ np.abs(down[0]).T
+    close(y, want, bound, 1.0, torch.bfloat16)
