@@ -8,10 +8,9 @@
 
 namespace {
 
-// Sizes below these keep every element offset inside int64 and every grid of
-// one workgroup per 16 entries inside the launch limit.
+// Operands of at most this many entries keep every offset and every count of workgroups
+// inside int64; whether the workgroups fit one launch is for the launch functions (grid_fits).
 constexpr int64_t kMaxEntries = int64_t(1) << 40;
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
 
 bool misaligned(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
@@ -44,8 +43,6 @@ int tsenor_quant_fp8(const void* X, int dtype, int64_t rows, int64_t cols, int64
     if (misaligned(values, 16) || misaligned(values_t, 16) || misaligned(X, element_size(dtype)))
         return TSENOR_ERR_SHAPE;
     if (rows == 0) return TSENOR_OK;
-    if (rows * blocks128(cols) / 16 >= kMaxGrid || blocks128(rows) * blocks128(cols) > kMaxGrid)
-        return TSENOR_ERR_SHAPE;
     return status(tsenor::launch_quant_fp8(X, dtype == TSENOR_BF16, rows, cols, ldx, values, scales,
                                            values_t, scales_t, stream),
                   "quant_fp8 kernel launch");
@@ -69,7 +66,6 @@ int tsenor_compress24_fp8(const void* W, int dtype, int64_t batch, int64_t strid
         misaligned(bad, 4) || misaligned(bad_t, 4))
         return TSENOR_ERR_SHAPE;
     if (batch == 0) return TSENOR_OK;
-    if (blocks128(rows) * blocks128(cols) > kMaxGrid / batch) return TSENOR_ERR_SHAPE;
     return status(tsenor::launch_compress24_fp8(W, dtype == TSENOR_BF16, batch, stride, rows, cols, ld,
                                                 mask, values, meta, scales, values_t, meta_t, scales_t,
                                                 bad, bad_t, stream),
@@ -91,7 +87,6 @@ int tsenor_spmm24_fp8(const void* X, int xtype, const uint8_t* xscales, int64_t 
     if (misaligned(values, 16) || misaligned(meta, 16) || misaligned(Y, element_size(ytype)))
         return TSENOR_ERR_SHAPE;
     if (n == 0) return TSENOR_OK;
-    if ((m + 15) / 16 > kMaxGrid / ((n + 15) / 16)) return TSENOR_ERR_SHAPE;
     return status(tsenor::launch_spmm24_fp8(X, xtype == TSENOR_BF16, xscales, n, ldx, values, meta, scales,
                                             m, k, Y, ytype == TSENOR_BF16, ldy, stream),
                   "spmm24_fp8 kernel launch");
@@ -107,7 +102,6 @@ int tsenor_gemm_fp8(const uint8_t* A, const uint8_t* a_scales, int64_t p, const 
         return TSENOR_ERR_SHAPE;
     if (misaligned(A, 16) || misaligned(B, 16) || misaligned(mask, 4) || misaligned(C, element_size(ctype)))
         return TSENOR_ERR_SHAPE;
-    if ((p + 15) / 16 > kMaxGrid / ((q + 15) / 16)) return TSENOR_ERR_SHAPE;
     return status(tsenor::launch_gemm_fp8(A, a_scales, p, B, b_scales, q, k, mask, C, ctype == TSENOR_BF16,
                                           ldc, stream),
                   "gemm_fp8 kernel launch");
@@ -136,7 +130,6 @@ static int moe_check(int64_t n, int64_t d, int64_t f, int64_t experts, int topk)
     if (n < 0 || n > 64 || d <= 0 || f <= 0 || d > (1 << 20) || f > (1 << 20) || too_big(experts * 128, d + 128) ||
         too_big(experts * 128, f + 128) || too_big(experts * (d + 128), f + 128))
         return TSENOR_ERR_SHAPE;
-    if (experts * ((f + 15) / 16) > kMaxGrid) return TSENOR_ERR_SHAPE;
     return TSENOR_OK;
 }
 

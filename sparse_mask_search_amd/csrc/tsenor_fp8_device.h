@@ -14,8 +14,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kBlock = 128;  // entries that share a scale along a row
-
 __host__ __device__ __forceinline__ int64_t pad128(int64_t k) { return (k + 127) / 128 * 128; }
 
 __device__ __forceinline__ float bits_float(uint32_t b) { return __builtin_bit_cast(float, b); }

@@ -57,3 +57,26 @@ def test_outputs_over_operands_are_found():
     assert not _refused(out, flat[144:176].view(4, 8))
     assert _refused(out, flat[144:200].view(7, 8))
     assert not _refused(out, flat[:0].view(1, 0))
+
+
+def test_messages_name_the_arguments():
+    from sparse_mask_search_amd import TsenorError
+    assert "topk" in str(TsenorError(4, "tsenor_moe24_fp8"))
+    assert "TSENOR_E4M3" in str(TsenorError(5, "tsenor_spmm24_fp8"))
+    assert "tau" in str(TsenorError(4, "tsenor_mask"))
+
+
+@pytest.mark.parametrize("name,args", [
+    ("quant", dict(rows=1 << 32, cols=128, ld=128, vt=None, st=None)),
+    ("quant", dict(rows=1 << 32, cols=1, ld=1)),
+    ("compress", dict(batch=1 << 25, stride=4096, rows=4, cols=4, ld=4)),
+    ("spmm", dict(n=1 << 20, m=1 << 20, ldy=1 << 20)),
+    ("spmm", dict(n=1 << 35, m=8, ldy=8)),
+    ("gemm", dict(p=1 << 20, q=1 << 20, k=1, ldc=1 << 20)),
+    ("gemm", dict(p=1 << 32, q=60, k=0, ldc=64)),
+])
+def test_grids_of_the_largest_operands(name, args):
+    """Operands of up to 2^40 entries whose workgroups do not fit one launch are refused on the host
+    (no launch is made here: the pointers are not device memory)."""
+    import test_fp8_abi as abi
+    assert getattr(abi, name)(**args) == abi.SHAPE
