@@ -177,3 +177,42 @@ def test_moe_scales_at_the_ends(which, byte):
         dh = 1.1 * reach * np.abs(u) if which == "gate" else reach * np.abs(silu)
         bound = bound + dh @ np.abs(down[0]).T
     close(y, want, bound, 1.0, torch.bfloat16)
+
+
+# ---- routing with experts that give no number -------------------------------------------
+
+@pytest.mark.parametrize("e", [6, 70, 300])
+def test_moe_experts_of_nan_logits_come_last(e):
+    import torch
+    rng = np.random.default_rng(e)
+    n, d, f = 5, 64, 64
+    gate, up, down = (_experts(rng, 6, f, d)[0] for _ in range(3))
+    at = torch.arange(e, device="cuda") % 6
+    part = lambda t: t.view(torch.uint8)[at].view(t.dtype)
+    gate, up, down = (a._replace(values=part(a.values), meta=a.meta[at], scales=part(a.scales)) for a in (gate, up, down))
+    x, _ = tensor(rng.standard_normal((n, d)), "bf16")
+    r, _ = tensor(rng.standard_normal((e, d)), "bf16")
+    y, ids, wts = sms.moe24_fp8(x, r, gate, up, down, 3, return_routing=True)
+    sync()
+    bad = [i for i in range(e) if i not in ids.unique().tolist()][:2]
+    if e == 6 and len(bad) < 2:       # few experts: leave three of them numbers
+        bad = [1, 2, 4]
+    whole = r.clone()
+    r[bad] = float("nan")
+    y2, ids2, wts2 = sms.moe24_fp8(x, r, gate, up, down, 3, return_routing=True)
+    sync()
+    logits = f64(x) @ np.nan_to_num(f64(r)).T
+    logits[:, bad] = -np.inf
+    assert np.array_equal(ids2.cpu().numpy(), np.argsort(-logits, axis=1, kind="stable")[:, :3])
+    assert bool(torch.isfinite(wts2).all()) and bool(torch.isfinite(y2).all())
+    if e > 6:
+        assert torch.equal(y2, y) and torch.equal(ids2, ids) and torch.equal(wts2, wts)
+    # more chosen than there are numbers: the numbers first, then the lowest of the others
+    keep, r = [0, 3], whole.clone()
+    r[[i for i in range(e) if i not in keep]] = float("nan")
+    _, ids3, wts3 = sms.moe24_fp8(x, r, gate, up, down, 4, return_routing=True)
+    sync()
+    order = np.argsort(-(f64(x) @ f64(whole).T)[:, keep], axis=1, kind="stable")
+    assert np.array_equal(ids3[:, :2].cpu().numpy(), np.array(keep)[order])
+    assert ids3[:, 2:].tolist() == [[1, 2]] * n
+    assert bool(torch.isnan(wts3).all())
