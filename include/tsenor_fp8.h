@@ -80,7 +80,7 @@ int tsenor_compress24_fp8(const void* W, int dtype, int64_t batch, int64_t strid
  * whose factor is below 2^-149, or 2^100 below another's in the same row of Y,
  * may be lost.)  The 8-bit matrix cores add eight products at a time
  * and drop what lies more than about 2^-12 below the largest of the eight; for
- * entries of similar size a sum is good to about 2^-16.  Entries that the mask
+ * entries of similar size a sum is good to about 2^-15.  Entries that the mask
  * removed are not multiplied, but the unused slots of a group with fewer than two
  * kept entries are: zeros times the entries of X at the positions 0 and 1 of an empty
  * group, at 3 beside one kept entry (2 if that is itself at 3).  A NaN there makes

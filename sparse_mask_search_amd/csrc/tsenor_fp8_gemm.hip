@@ -69,12 +69,13 @@ __device__ __forceinline__ i32x8 quant_fragment(const uint16_t* row, int64_t k0,
     return i32x8{(int)a.x, (int)a.y, (int)b.x, (int)b.y, (int)c.x, (int)c.y, (int)d.x, (int)d.y};
 }
 
-// Few tokens (n <= 16 NT): reading A bounds the product (1 token, 28672 x 8192: 147 MB in 29 us,
-// 5.1 TB/s; 1 token, 4096 x 4096: 4.0 us, of which some 2 are the launch), so a workgroup owns 16 MT
-// rows of A and each of its eight waves a stretch of k, with the loads of kAhead
-// blocks in flight (stretches, not blocks in turn: the workgroup then reads whole rows
-// at a time, over all memory channels); the waves' sums meet in LDS, in wave order.  QX: X
-// is bf16 and quantised on the way.
+// Few tokens (n <= 16 NT): reading A bounds the product, so a workgroup owns 16 MT rows of A
+// and each of its eight waves a stretch of k, with the loads of kAhead blocks in flight
+// (stretches, not blocks in turn: the workgroup then reads whole rows at a time, over all
+// memory channels); the waves' sums meet in LDS, in wave order.  QX: X is bf16 and quantised
+// on the way, by each workgroup for itself between its loads of A.  One quantised token,
+// 28672 x 8192: 147 MB in 35 us, 4.2 TB/s (29 us with A in the last-level cache), from bf16
+// 50; 4096 x 4096: 5 us, of which some 2 are the launch, from bf16 7.5.
 constexpr int kFewWaves = 8;
 
 template <int NT, int MT, bool QX, class TY>
@@ -238,10 +239,10 @@ constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside
 // 2^e for e <= 127; 0 below 2^-126.
 __device__ __forceinline__ float power(int e) { return bits_float(e < -126 ? 0u : (uint32_t)(127 + e) << 23); }
 
-// Y = X A^T (A on the rows of the instruction).  8192 x 28672 x 8192 in 1.43 ms: 2.7 PFLOP/s
-// dense-equivalent, of 8.3 that the instruction reaches in registers.  Neither the matrix cores
-// (1024 of some 3300 cycles a step) nor the VALU (160 instructions a wave) nor L2 bound it
-// alone: the eight waves of the one workgroup that fits a CU go through the same phases (wait,
+// Y = X A^T (A on the rows of the instruction).  8192 x 28672 x 8192 in 1.39 to 1.48 ms, by
+// the card's clock: 2.6 to 2.8 PFLOP/s dense-equivalent, of 8.3 that the instruction reaches
+// in registers.  Neither the matrix cores (1024 of some 3300 cycles a step) nor the VALU (160
+// instructions a wave) nor L2 bound it alone: the eight waves of the one workgroup that fits a CU go through the same phases (wait,
 // LDS reads, multiply) together, and the clock is at 2 GHz under the load.
 template <int TM, int TN, int WM, int WN, int R, class TY>
 __global__ __launch_bounds__(64 * WM * WN) void spmm24_fp8_tile_kernel(
@@ -595,9 +596,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_tile_kernel(
 // run, so the barrier that publishes the next buffer stands in the middle of a step, where
 // no wave waits for LDS.  The matrix cores are busy 64% of the time (51% with whole blocks
 // per step and the barrier at its start); the clock falls from 1.94 to 1.76 GHz with it, so
-// that the power limit takes back most of the gain: 8192^3 504 -> 475 us, 2.3 PFLOP/s.
-// Four waves of 128 x 128 measured 490 us; smaller tiles are slower in this form (128 x 128
-// at 8192 x 4096 x 8192: 352 us against 290).
+// that the power limit takes back most of the gain: 8192^3 504 -> 475 us on one card, 2.3
+// PFLOP/s (445 to 450 on others, where a dense library product takes 360).  Four
+// waves of 128 x 128 measured 490 us; smaller tiles are slower in this form (128 x 128 at
+// 8192 x 4096 x 8192: 352 us against 290).
 template <int TM, int TN, int WM, int WN, int R, class TC>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_fp8_wide_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t p,

@@ -8,9 +8,10 @@
 // Reading the chosen experts' weights bounds the layer, so a workgroup's four
 // waves share the reduction out in stretches and keep several blocks' loads in
 // flight; the waves' sums meet in LDS in wave order, without atomics.  33 tokens, 4 of 16
-// experts, 4096 x 2048: hidden 38 us for 168 MB (4.4 TB/s), down 25 us for 84 MB (3.4 TB/s),
-// logits, route and sum 16 us together; one token, 6 of 64, 2048 x 1408: 9.9 + 5.4 + 10.8 us, where
-// the five launches and their dependent loads count more than the 32 MB.
+// experts, 4096 x 2048, over weights in turn: hidden 43 us for 168 MB (3.9 TB/s), down 27 us for
+// 84 MB (3.1 TB/s), logits, route and sum 16 us together (38, 25 and 16 with the same weights
+// again, in part from the last-level cache); one token, 6 of 64, 2048 x 1408: 10.8 + 5.8 + 10.4
+// us, where the five launches and their dependent loads count more than the 32 MB.
 // The hidden entries are kept as the sum of two bf16 numbers (16 fraction bits;
 // one alone would lose as much as the rounding of y itself), which costs two more
 // matrix instructions per block where the memory is waited for.

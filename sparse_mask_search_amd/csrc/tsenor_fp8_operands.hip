@@ -13,7 +13,8 @@ namespace {
 using namespace fp8;
 
 // Along the rows only: 16 lanes hold one block of 128 (8 entries each).  Bound by memory:
-// 4096 x 11008 bf16 in 25 us (5.4 TB/s read and written).
+// 4096 x 11008 bf16 in 28 us (4.8 TB/s read and written; 25 us where the last-level cache still
+// holds the input).  f32: 37 us.
 template <class T>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ X, int64_t rows,
                                                          int64_t cols, int64_t ldx, bool vec,
@@ -39,7 +40,8 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T* __restrict__ X
 // column (f32: 64 rows) or of two (bf16: 32 rows of a pair, one LDS word a row) in registers;
 // the 8-bit columns leave through LDS, so that eight lanes write the 128 bytes of a column
 // side by side (written by the threads that hold them, each store would touch 64 lines).
-// Both ways, 4096 x 11008 bf16: 34 us, 5.3 TB/s.
+// Both ways, 4096 x 11008 bf16: 40 us, 4.6 TB/s (34 us with the input in the last-level cache);
+// along the columns only 32.  f32, whose tile takes twice the LDS: 68 us, 4.0 TB/s; columns only 57.
 template <class T>
 __global__ __launch_bounds__(256) void quant_tile_kernel(const T* __restrict__ X, int64_t rows,
                                                          int64_t cols, int64_t ldx, bool vec,
@@ -156,10 +158,10 @@ __device__ __forceinline__ uint32_t take_two(uint32_t a, uint32_t qa, uint32_t b
 // give the one scale that both orientations share.  The rows are compressed from the
 // registers that hold them (16 lanes a row, two groups each); for the columns the 8-bit
 // numbers go to LDS, a thread turns 4 x 4 cells of them around with byte permutations, and
-// the compressed columns leave through LDS as whole lines.  11008 x 4096 bf16 both ways: 43 us
-// for 152 MB; some 1000 VALU instructions a thread keep it from the memory's rate.
-// 8192 x 8192 f32: 83 us for 361 MB.  The compressed columns take the tile's place in LDS (19.5 KB
-// in all against 29), which is worth 4 to 8%.
+// the compressed columns leave through LDS as whole lines.  11008 x 4096 bf16 both ways: 48 us
+// for 152 MB (42 with the input in the last-level cache; one way 33 to 37); some 1000 VALU
+// instructions a thread keep it from the memory's rate.  8192 x 8192 f32: 80 us for 361 MB.  The
+// compressed columns take the tile's place in LDS (19.5 KB in all against 29), which is worth 4 to 8%.
 template <class T>
 __global__ __launch_bounds__(256) void compress24_fp8_kernel(
     const T* __restrict__ W, int64_t stride, int64_t rows, int64_t cols, int64_t ld, bool vec,
