@@ -188,3 +188,64 @@ def test_gemm_nan_is_masked(p, q, k):
     want = av @ bv.T * keep
     want[3, keep[3]] = np.nan
     assert np.array_equal(f64(c), want, equal_nan=True)
+
+
+# ---- operands of odd sizes ------------------------------------------------------------------
+
+def odd_operand(rng, m, k):
+    """An operand of any size, from one whose size compression takes: the rows behind m are cut off,
+    the columns behind k are removed by the mask.  Its masked values."""
+    mm, kk = -(-m // 4) * 4, -(-k // 4) * 4
+    w, keep, _ = exact_weight(rng, mm, kk)
+    keep[:, k:] = False
+    A, bad = sms.compress24_fp8(w, words(keep))
+    assert int(bad.item()) == 0
+    wv = (f64(w) * keep)[:m, :k]
+    return sms.Sparse24Fp8(A.values[:m], A.meta[:m], A.scales[:-(-m // 128)], k), wv
+
+
+@pytest.mark.parametrize("m,k", [(1, 1), (3, 127), (67, 129), (131, 259), (1001, 515), (4101, 261)])
+def test_spmm_odd_sizes_exact(m, k):
+    import torch
+    rng = np.random.default_rng(m + k)
+    A, wv = odd_operand(rng, m, k)
+    for n in (1, 5, 16, 33, 65, 301) + ((4099,) if m > 4000 else ()):
+        say("spmm odd", n, m, k)
+        x, xv = tensor(integers(rng, (n, k), 7) * powers(rng, n, k, 1), "bf16")
+        want = exact_product(xv, wv)
+        for X in (x, sms.quant_fp8(x)):
+            for dt, off in ((torch.float32, 1), (torch.bfloat16, 0)):
+                buf = torch.full((n + 2, m + 3), 7.0, dtype=dt, device="cuda")
+                y = buf[1:n + 1, off:off + m]
+                sms.spmm24_fp8(X, A, out=y)
+                sync()
+                assert torch.equal(y, want.to(torch.float32).to(dt))
+                y.fill_(7.0)
+                assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("n,d,f,e,topk", [(1, 1, 1, 1, 1), (3, 67, 33, 3, 2), (20, 129, 131, 4, 3), (5, 1031, 517, 9, 4)])
+def test_moe_odd_sizes(n, d, f, e, topk):
+    import torch
+    say("moe odd", n, d, f, e, topk)
+    rng = np.random.default_rng(n + d + f)
+
+    def stack(m, k):
+        ops = [odd_operand(rng, m, k) for _ in range(e)]
+        st = lambda i: torch.stack([(o[i] if i == 1 else o[i].view(torch.uint8)) for o, _ in ops])
+        return (sms.Sparse24Fp8(st(0).view(torch.float8_e4m3fn), st(1), st(2).view(torch.float8_e8m0fnu), k),
+                np.stack([v for _, v in ops]))
+
+    (gate, gd), (up, ud), (down, dd) = stack(f, d), stack(f, d), stack(d, f)
+    x, xv = tensor(2.0 ** -6 * rng.standard_normal((n, d)), "bf16")
+    r, rv = tensor(rng.standard_normal((e, d)), "bf16")
+    buf = torch.full((n + 2, d + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = buf[1:n + 1, 1:d + 1]
+    _, ids, wts = sms.moe24_fp8(x, r, gate, up, down, topk, out=y, return_routing=True)
+    sync()
+    wi, ww = _route(xv, rv, topk)
+    assert np.array_equal(ids.cpu().numpy(), wi)
+    want, bound = _moe_reference(xv, wi, ww, gd, ud, dd)
+    close(y, want, bound, 1.0, torch.bfloat16)
+    y.fill_(7.0)
+    assert bool((buf == 7.0).all())
