@@ -18,8 +18,11 @@ from ._lib import (F32, BF16, TsenorError, compress24, exact, lib, library_path,
                    mask_batched, mask_noalloc, memory_pass, round_mask, spmm24, unpack, version)
 from ._fp8 import (DenseFp8, Sparse24Fp8, compress24_fp8, compress24_fp8_both, gemm_fp8,
                    moe24_fp8, quant_fp8, quant_fp8_both, spmm24_fp8)
+from ._ops import (DenseInt8, clip_grads, gemm_int8, grad_norm, grouped_mm, grouped_wgrad,
+                   quant_int8)
 
 __all__ = ["F32", "BF16", "TsenorError", "compress24", "exact", "lib", "library_path", "mask",
            "mask_batched", "mask_noalloc", "memory_pass", "round_mask", "spmm24", "unpack",
            "version", "DenseFp8", "Sparse24Fp8", "compress24_fp8", "compress24_fp8_both",
-           "gemm_fp8", "moe24_fp8", "quant_fp8", "quant_fp8_both", "spmm24_fp8"]
+           "gemm_fp8", "moe24_fp8", "quant_fp8", "quant_fp8_both", "spmm24_fp8", "DenseInt8",
+           "clip_grads", "gemm_int8", "grad_norm", "grouped_mm", "grouped_wgrad", "quant_int8"]

@@ -57,7 +57,7 @@ def _placed(fn):
         if not args and first not in kw:
             raise TypeError(f"{fn.__name__}() missing required argument: '{first}'")
         x = args[0] if args else kw[first]
-        t = x.values if isinstance(x, (DenseFp8, Sparse24Fp8)) else x
+        t = x[0] if isinstance(x, (tuple, list)) and x else x  # an operand's values, the first of a list
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{fn.__name__} needs CUDA (HIP) torch tensors")
         device = t.device

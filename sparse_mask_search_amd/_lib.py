@@ -82,6 +82,23 @@ def lib():
                                        _P, _P, _P, _P, _I64, _P, ctypes.c_size_t, _P, _I64, _P, _P,
                                        _P]
         l.tsenor_moe24_fp8.restype = _I
+        l.tsenor_grouped_mm.argtypes = [_P, _I64, _I64, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _I,
+                                        _I64, _P]
+        l.tsenor_grouped_mm.restype = _I
+        l.tsenor_grouped_wgrad.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I,
+                                           _I64, _I64, _P]
+        l.tsenor_grouped_wgrad.restype = _I
+        l.tsenor_quant_int8.argtypes = [_P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P]
+        l.tsenor_quant_int8.restype = _I
+        l.tsenor_gemm_int8.argtypes = [_P, _I, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _I, _I64,
+                                       _P]
+        l.tsenor_gemm_int8.restype = _I
+        l.tsenor_grads_workspace.argtypes = [_I]
+        l.tsenor_grads_workspace.restype = ctypes.c_size_t
+        l.tsenor_grad_norm.argtypes = [_P, _I, _P, ctypes.c_size_t, _P, _P]
+        l.tsenor_grad_norm.restype = _I
+        l.tsenor_clip_grads.argtypes = [_P, _I, _F, _P, ctypes.c_size_t, _P, _P]
+        l.tsenor_clip_grads.restype = _I
         l.tsenor_status_str.argtypes = [_I]
         l.tsenor_status_str.restype = ctypes.c_char_p
         l.tsenor_last_error.argtypes = []

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtsenor.so")
 SOURCES = ["tsenor_abi.cpp", "tsenor_kernels.hip", "tsenor_spmm.hip", "tsenor_bench.hip",
            "tsenor_fp8_abi.cpp", "tsenor_fp8_operands.hip", "tsenor_fp8_gemm.hip",
-           "tsenor_fp8_moe.hip"]
+           "tsenor_fp8_moe.hip", "tsenor_ops_abi.cpp", "tsenor_grouped.hip", "tsenor_int8.hip",
+           "tsenor_grads.hip"]
 ARCH = os.environ.get("TSENOR_OFFLOAD_ARCH", "gfx950")
 
 

@@ -592,8 +592,8 @@ const char* tsenor_status_str(int status) {
         case TSENOR_ERR_NULL: return "required pointer is NULL";
         case TSENOR_ERR_SHAPE: return "bad shape, leading dimension or alignment (masks: rows/cols positive multiples of M, ld >= cols)";
         case TSENOR_ERR_NM: return "bad N:M (M in {4,8,16,32}, 1 <= N <= M)";
-        case TSENOR_ERR_PARAM: return "bad parameter (masks: tau finite >= 0, iters >= 1, ls_steps >= 0; experts: 1 <= topk <= min(16, experts), experts <= 512)";
-        case TSENOR_ERR_DTYPE: return "bad dtype (TSENOR_F32, TSENOR_BF16, or where an operand allows it TSENOR_E4M3)";
+        case TSENOR_ERR_PARAM: return "bad parameter (masks: tau finite >= 0, iters >= 1, ls_steps >= 0; experts: 1 <= topk <= min(16, experts), experts <= 512; grouped products: 1 <= experts <= 1024; gradients: count, max_norm >= 0)";
+        case TSENOR_ERR_DTYPE: return "bad dtype (TSENOR_F32, TSENOR_BF16, or where an operand allows it TSENOR_E4M3, TSENOR_INT8)";
         case TSENOR_ERR_HIP: return "HIP runtime error (see tsenor_last_error)";
         case TSENOR_ERR_NONFINITE: return "input holds a non-finite value (TSENOR_DEBUG_CHECKS=1)";
         default: return "unknown status";

@@ -1,0 +1,224 @@
+// tsenor_ops_device.h -- device helpers of the grouped and 8-bit integer
+// products: matrix instructions, LDS tiles and their fragments, rows of experts.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tsenor_fp8_device.h"
+#include "tsenor_ops_internal.h"
+
+namespace tsenor {
+namespace ops {
+
+using namespace fp8;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// One matrix instruction takes 16 bytes of the reduction from each lane half h = lane / 32:
+// A row lane % 32, B column lane % 32; result column lane % 32, rows 8 i0 + 4 h + i1 in
+// register 4 i0 + i1.  32 bytes of a row in all: 16 bf16 or 32 integers.
+struct Bf16 {
+    static constexpr int kSize = 2;
+    typedef f32x16 Sum;
+    typedef f32x4 Sum4;
+    __device__ static __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+    __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+};
+struct Int8 {
+    static constexpr int kSize = 1;
+    typedef i32x16 Sum;
+    typedef i32x4 Sum4;
+    __device__ static __forceinline__ i32x16 mma(u32x4 a, u32x4 b, i32x16 c) {
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
+                                                     0, 0, 0);
+    }
+    __device__ static __forceinline__ i32x4 mma(u32x4 a, u32x4 b, i32x4 c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
+                                                     0, 0, 0);
+    }
+};
+
+// LDS tiles of one step, 64 bytes of the reduction for `W` rows or columns, in chunks of 16
+// bytes.  An operand that is contiguous along the reduction is kept by rows of 64 bytes, chunk c of
+// row r at c ^ ((r >> 2) & 3): the 16 rows of one pass of a 16-byte read then hit different
+// banks.  One that is contiguous along its columns (bf16) is kept as it lies, 32 rows of the
+// reduction of W entries, and turned by the transposing read below; pairs of chunks are moved
+// so that the four rows of such a read hit different banks.
+__device__ __forceinline__ int row_slot(int r, int c) { return 4 * r + (c ^ ((r >> 2) & 3)); }
+template <int W>
+__device__ __forceinline__ int turned_slot(int r, int c) {  // chunk c of reduction row r
+    constexpr int kChunks = W / 8;
+    const int f = W >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1);
+    return kChunks * r + (c ^ f);
+}
+
+// Fragment kc (0, 1) of rows row0 .. row0 + 31: chunk 2 kc + h of row lane % 32.
+__device__ __forceinline__ u32x4 row_fragment(const u32x4* tile, int row0, int kc, int lane) {
+    return tile[row_slot(row0 + (lane & 31), 2 * kc + (lane >> 5))];
+}
+// The same of a column-contiguous tile.  ds_read_b64_tr_b16, for each 16 lanes: lane i gives the
+// address of 4 entries, of row i / 4 and columns 4 (i % 4) ..; it receives column i of the four
+// rows (probed).  Two such reads give a lane the eight reduction entries of its column.
+template <int W>
+__device__ __forceinline__ u32x4 turned_fragment(const u32x4* tile, int col0, int kc, int lane) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const int g = lane >> 4, i = lane & 15;
+    const int row = 16 * kc + 8 * (g >> 1) + (i >> 2), chunk = (col0 >> 3) + 2 * (g & 1) + ((i & 3) >> 1);
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(tile) + 8 * (i & 1);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + 16 * turned_slot<W>(row, chunk)));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + 16 * turned_slot<W>(row + 4, chunk)));
+    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+    return u32x4{a.x, a.y, b.x, b.y};
+}
+
+// Where the rows of one tile lie.
+struct RowTile {
+    int expert;      // -1: rows of no expert
+    int first, end;  // rows first .. min(first + tile, end) - 1
+};
+
+// An entry of `ends` as it counts.
+__device__ __forceinline__ int end_of(const int* ends, int e, int rows) { return min(max(ends[e], 0), rows); }
+
+// Tiles of `size` rows, expert after expert, then those of no expert: tile t, or their number
+// in *tiles when t < 0 (64 experts at a time, one a lane).  Every lane gets the same answer.
+__device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows, int size, int t, RowTile* to,
+                                         int* tiles = nullptr) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, last = 0;
+    if (ends == nullptr) {
+        before = (rows + size - 1) / size;
+        last = rows;
+        if (t >= 0 && t < before) {
+            *to = {0, t * size, rows};
+            return true;
+        }
+    } else {
+        for (int e0 = 0; e0 < experts; e0 += 64) {
+            const int e = e0 + lane;
+            const int hi = e < experts ? end_of(ends, e, rows) : 0;
+            int lo = __shfl_up(hi, 1, 64);
+            if (lane == 0) lo = last;
+            const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(sum, d, 64);
+                if (lane >= d) sum += o;
+            }
+            const uint64_t behind = __ballot(t >= 0 && before + sum > t);
+            if (behind != 0) {
+                const int l = __builtin_ctzll(behind);
+                const int start = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(n, l);
+                const int first = __builtin_amdgcn_readlane(lo, l);
+                *to = {e0 + l, first + (t - start) * size, __builtin_amdgcn_readlane(hi, l)};
+                return true;
+            }
+            before += __builtin_amdgcn_readlane(sum, 63);
+            last = __builtin_amdgcn_readlane(hi, min(63, experts - 1 - e0));
+        }
+    }
+    if (tiles != nullptr) *tiles = before + (rows - last + size - 1) / size;
+    if (t < 0) return false;
+    *to = {-1, last + (t - before) * size, rows};
+    return to->first < rows;
+}
+
+// The most tiles that row_tile can give.
+inline int64_t most_row_tiles(int64_t rows, int64_t experts, int64_t size, bool grouped) {
+    return grouped ? rows / size + (experts + 1 < rows ? experts + 1 : rows) : (rows + size - 1) / size;
+}
+
+// ---- 8-bit integers --------------------------------------------------------
+//
+// q = nearest-even(x * 127 / amax), as if taken exactly.  With x = X 2^a, amax = M 2^b, X and
+// M integers below 2^p (p = 8 for bf16, 24 for fp32), x * 127 / amax is a half h / 2 exactly or
+// off it by |254 X - h M 2^(b-a)| / (254 X) >= 1 / (254 X) > 2^-(p+8) of its value (the numerator is
+// a multiple of 2^min(0, b-a), and where b < a, M 2^(b-a) < 2^p takes X's place likewise).  The
+// quotient computed as x * (127 / amax) is off by less than 2 half steps: 2^-23 in fp32, 2^-52 in
+// fp64.  So a computed value within 2^-20 (bf16 in fp32; 2^-16 apart) or 2^-40 (fp32 in fp64; 2^-32
+// apart) of a half is that half, and goes to the even side; any other rounds the right way.
+
+struct TokenScale {
+    float factor;  // bf16: 127 / (amax * 2^-exponent), so that no quotient leaves fp32's range
+    int exponent;
+    float scale;   // amax / 127
+};
+// amax as fp32 bits; kSpecial or more: a row with an infinity or a NaN.
+__device__ __forceinline__ TokenScale token_scale(uint32_t amax) {
+    const float m = bits_float(amax);
+    if (amax >= kSpecial) return {0.f, 0, bits_float(0x7FC00000u)};
+    if (amax == 0u) return {0.f, 0, 0.f};
+    const int e = __builtin_amdgcn_frexp_expf(m);
+    return {127.f / __builtin_ldexpf(m, -e), e, m / 127.f};
+}
+// One entry as an integer (any where the row's factor is 0: see integers below).
+__device__ __forceinline__ int integer(float x, float factor, int exponent) {
+    const float t = __builtin_ldexpf(x, -exponent) * factor;
+    const float n = __builtin_rintf(t);
+    const bool half = __builtin_fabsf(__builtin_fabsf(t - n) - 0.5f) <= __builtin_fabsf(t) * 0x1p-20f;
+    return (int)(half ? 2.f * __builtin_rintf(0.5f * t) : n);
+}
+__device__ __forceinline__ int integer(float x, double factor) {
+    const double t = (double)x * factor, n = __builtin_rint(t);
+    const bool half = __builtin_fabs(__builtin_fabs(t - n) - 0.5) <= __builtin_fabs(t) * 0x1p-40;
+    return (int)(half ? 2.0 * __builtin_rint(0.5 * t) : n);
+}
+__device__ __forceinline__ uint32_t pack_integers(int a, int b, int c, int d) {
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+}
+// Eight bf16 entries; all 0 where the row's factor is 0.
+__device__ __forceinline__ u32x2 integers(const Eight<uint16_t>& v, float factor, int exponent) {
+    int n[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        n[2 * i] = integer(bits_float(v.w[i] << 16), factor, exponent);
+        n[2 * i + 1] = integer(bits_float(v.w[i] & 0xFFFF0000u), factor, exponent);
+    }
+    const u32x2 packed = {pack_integers(n[0], n[1], n[2], n[3]), pack_integers(n[4], n[5], n[6], n[7])};
+    return factor == 0.f ? u32x2{0u, 0u} : packed;
+}
+__device__ __forceinline__ u32x2 integers(const Eight<float>& v, double factor) {
+    int n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n[i] = integer(bits_float(v.w[i]), factor);
+    const u32x2 packed = {pack_integers(n[0], n[1], n[2], n[3]), pack_integers(n[4], n[5], n[6], n[7])};
+    return factor == 0.0 ? u32x2{0u, 0u} : packed;
+}
+// Largest value over the wave.
+__device__ __forceinline__ uint32_t max64(uint32_t v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v = max(v, (uint32_t)__shfl_xor(v, d, 64));
+    return v;
+}
+
+// Four neighbouring entries of an output row, columns c .. c+3 (< cols written).
+__device__ __forceinline__ void put4(float* y, int64_t c, int64_t cols, bool vec, f32x4 v) {
+    if (vec && c + 4 <= cols) {
+        *reinterpret_cast<f32x4*>(y + c) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < cols) y[c + i] = v[i];
+    }
+}
+__device__ __forceinline__ void put4(uint16_t* y, int64_t c, int64_t cols, bool vec, f32x4 v) {
+    if (vec && c + 4 <= cols) {
+        *reinterpret_cast<u32x2*>(y + c) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < cols) y[c + i] = to_bf16(v[i]);
+    }
+}
+
+}  // namespace ops
+}  // namespace tsenor
