@@ -35,6 +35,30 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* p, int64_t valid) {
     return v;
 }
 
+// Four neighbouring results of a lane, at columns c .. c + 3 of a row, scaled or masked, to `y`.
+template <class T, Kind K, class TO>
+__device__ __forceinline__ void finish(const GroupedJob& job, int expert, int64_t row, int64_t c, typename T::Sum sum,
+                                       TO* y) {
+    if (c >= job.inner) return;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)sum[e];
+    if constexpr (T::kSize == 1) {
+        const float scale = job.bs[row], *as = job.as + expert * job.inner;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = v[e] * scale * as[min(c + e, job.inner - 1)];
+    }
+    if constexpr (K == kGradient) {
+        if (job.mask != nullptr) {  // c is a multiple of four: one word
+            const uint32_t keep = job.mask[(expert * job.outer + row) * ((job.inner + 31) / 32) + (c >> 5)] >> (c & 31);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!((keep >> e) & 1u)) v[e] = 0.f;
+        }
+    }
+    put4(y, c, job.inner, job.ovec, v);
+}
+
 // Any alignment and any size: tiles of 64 x 64, four waves of 32 x 32, operands through
 // registers into two LDS buffers.  AT, BT: the operand is contiguous along its columns.
 template <class T, bool AT, bool BT, Kind K, class TO>
@@ -88,9 +112,9 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
         return load16<T>(base + r * ld + c * T::kSize, r * T::kSize < reduce ? (have - c) * T::kSize : 0);
     };
     const int slot_row = row_slot(tid >> 2, tid & 3), slot_turned = turned_slot<64>(tid >> 3, tid & 7);
-    typename T::Sum acc;
+    typename T::Sum acc[2][2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0;
+    for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = typename T::Sum{0, 0, 0, 0};
     u32x4 va, vb;
     if (steps > 0) {
         va = fetch(a, job.lda, ahave, AT, 0);
@@ -105,36 +129,23 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
             va = fetch(a, job.lda, ahave, AT, s + 1);
             vb = fetch(b, job.ldb, bhave, BT, s + 1);
         }
+        u32x4 fa[2], fb[2];
 #pragma unroll
-        for (int kc = 0; kc < 2; ++kc) {
-            const u32x4 fa = AT ? turned_fragment<64>(ta[s & 1], ia, kc, lane) : row_fragment(ta[s & 1], ia, kc, lane);
-            const u32x4 fb = BT ? turned_fragment<64>(tb[s & 1], ib, kc, lane) : row_fragment(tb[s & 1], ib, kc, lane);
-            acc = T::mma(fa, fb, acc);
+        for (int i = 0; i < 2; ++i) {
+            const int ra = ia + 16 * i, rb = ib + 16 * i;
+            fa[i] = AT ? turned_fragment<64>(ta[s & 1], ra, lane) : row_fragment(ta[s & 1], ra, lane);
+            fb[i] = BT ? turned_fragment<64>(tb[s & 1], rb, lane) : row_fragment(tb[s & 1], rb, lane);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = T::mma(fa[i >> 1], fb[i & 1], acc[i >> 1][i & 1]);
     }
-    const int64_t row = outer0 + ib + (lane & 31), c0 = inner0 + ia;
-    if (row >= outer_end || c0 >= job.inner) return;
-    uint32_t keep = 0xFFFFFFFFu;
-    if constexpr (K == kGradient) {
-        if (job.mask != nullptr) {
-            const int64_t wpr = (job.inner + 31) / 32;
-            keep = job.mask[(expert * job.outer + row) * wpr + (c0 >> 5)];
-        }
-    }
-    float scale = 1.f;
-    if constexpr (T::kSize == 1) scale = job.bs[row];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t c = c0 + 8 * i + 4 * (lane >> 5);
-        f32x4 v;
+    for (int j = 0; j < 2; ++j) {
+        const int64_t row = outer0 + ib + 16 * j + (lane & 15);
+        if (row >= outer_end) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = (float)acc[4 * i + e];
-            if constexpr (T::kSize == 1) v[e] = v[e] * scale * job.as[expert * job.inner + min(c + e, job.inner - 1)];
-            if constexpr (K == kGradient)
-                if (!((keep >> (8 * i + 4 * (lane >> 5) + e)) & 1u)) v[e] = 0.f;
-        }
-        put4(out + row * job.ldo, c, job.inner, job.ovec, v);
+        for (int i = 0; i < 2; ++i)
+            finish<T, K>(job, expert, row, inner0 + ia + 16 * i + 4 * (lane >> 4), acc[i][j], out + row * job.ldo);
     }
 }
 
@@ -150,7 +161,7 @@ constexpr int kFewWaves = 8;
 template <class T, bool QX, int NT, int MT, class TO>
 __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const GroupedJob job) {
     constexpr int kAhead = NT * MT >= 4 ? 1 : NT * MT >= 2 ? 2 : 4;
-    typedef typename T::Sum4 Sum4;
+    typedef typename T::Sum Sum4;
     __shared__ Sum4 sums[kFewWaves][MT * NT][64];
     __shared__ TokenScale scale[QX ? 16 : 1];
     __shared__ uint32_t part[QX ? 16 : 1][kFewWaves];
@@ -290,6 +301,266 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
     }
 }
 
+// ---- tiles fed by direct loads -------------------------------------------------
+//
+// A workgroup of WM x WN waves owns TM inner columns x TN rows of the output, a wave (TM / WM) x
+// (TN / WN) in tiles of 32 x 32, and walks the reduction in steps of 64 bytes.  Operands reach LDS by
+// direct loads (no registers between) into a ring of R buffers filled R - 1 steps ahead.
+// The operands of the next step's first instructions are read while this step's last ones run,
+// so the barrier that publishes the next buffer stands in the middle of a step, where no wave
+// waits for LDS; loads go out one by one between the matrix instructions, since all at once they
+// would stall every wave on the address unit.  Rows and columns behind an operand's end
+// repeat its last one (nothing of them is stored); behind the reduction's end zeros are loaded.
+
+constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside a tile fit 32 bits
+
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
+
+// Direct load from a lane's own address (the steps with an end of the reduction).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16_at(const void* p, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds_base)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// One operand of a tile, `S` rows (or columns) wide, as its direct loads see it.
+template <class T, bool TURNED, int S, int WAVES>
+struct Loads {
+    static constexpr int kCount = S / 16 / WAVES;  // of a wave per step, 1024 bytes each
+    static_assert(kCount * 16 * WAVES == S, "tile");
+    const uint8_t* base;      // the tile's first entry
+    int64_t step;             // bytes from step to step
+    uint32_t offset[kCount];  // of this lane
+    // have: rows (columns) of the tile that exist
+    __device__ __forceinline__ void init(const uint8_t* first, int64_t ld, int have, int wave, int lane) {
+        base = uniform(first);
+        step = TURNED ? 32 * ld : 64;
+#pragma unroll
+        for (int j = 0; j < kCount; ++j) {
+            const int slot = 64 * (wave * kCount + j) + lane;
+            if constexpr (TURNED) {
+                const int r = slot / (S / 8), c = turned_slot<S>(r, slot % (S / 8)) - r * (S / 8);
+                offset[j] = __umul24(r, (uint32_t)ld) + 16 * min(c, (have - 1) / 8);
+            } else {
+                const int r = slot / 4, c = row_slot(r, slot % 4) - 4 * r;
+                offset[j] = __umul24(min(r, have - 1), (uint32_t)ld) + 16 * c;
+            }
+        }
+    }
+    __device__ __forceinline__ void load(int j, int64_t s, const u32x4* tile, int wave) const {
+        dma16(base + s * step, offset[j], lds_offset(tile + 64 * (wave * kCount + j)));
+    }
+    // the same with zeros behind the reduction's `reduce` bytes (turned: of one column)
+    __device__ __forceinline__ void load_end(int j, int64_t s, int64_t reduce, const u32x4* tile, int wave,
+                                             int lane) const {
+        const int slot = 64 * (wave * kCount + j) + lane;
+        int64_t at;
+        if constexpr (TURNED) {
+            at = (32 * s + slot / (S / 8)) * T::kSize;
+        } else {
+            const int r = slot / 4;
+            at = 64 * s + 16 * (row_slot(r, slot % 4) - 4 * r);
+        }
+        const uint8_t* p = at < reduce ? base + s * step + offset[j] : reinterpret_cast<const uint8_t*>(&kZeros);
+        dma16_at(p, lds_offset(tile + 64 * (wave * kCount + j)));
+    }
+    __device__ static __forceinline__ u32x4 fragment(const u32x4* tile, int at, int lane) {
+        if constexpr (TURNED) return turned_fragment<S>(tile, at, lane);
+        else return row_fragment(tile, at, lane);
+    }
+};
+
+// Work t of `count` for workgroup `bid`: workgroups go to the chip's 8 XCDs round robin and each
+// XCD has its own L2, so XCD x gets a contiguous range.
+__device__ __forceinline__ int64_t in_order(int64_t bid, int64_t count) {
+    const int64_t x = bid % 8, rest = count % 8;
+    return x * (count / 8) + (x < rest ? x : rest) + bid / 8;
+}
+// Tile t of a grid, in groups of up to 8 tm column by column: a range forms a compact block.
+__device__ __forceinline__ void grid_tile(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
+    const int64_t grp = t / (8 * tiles_n), first = grp * 8, gm = min(tiles_m - first, (int64_t)8);
+    const int64_t r = t - grp * 8 * tiles_n;
+    tm = first + r % gm;
+    tn = r / gm;
+}
+
+// Whether a step's loads may meet the reduction's end.
+struct Inside {
+    static constexpr bool value = false;
+};
+struct AtEnd {
+    static constexpr bool value = true;
+};
+
+template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, class TO>
+__global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const GroupedJob job) {
+    constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
+    typedef Loads<T, AT, TM, W> LoadsA;
+    typedef Loads<T, BT, TN, W> LoadsB;
+    static_assert(R >= 3, "ring");
+    struct Buffer {
+        u32x4 a[TM * 4];
+        u32x4 b[TN * 4];
+    };
+    __shared__ Buffer ring[R];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int64_t across = (job.inner + TM - 1) / TM;
+    const uint8_t *a = static_cast<const uint8_t*>(job.a), *b = static_cast<const uint8_t*>(job.b);
+    TO* out = static_cast<TO*>(job.out);
+    int64_t inner0, outer0, outer_end, reduce, tm, tn;
+    int expert;
+    if constexpr (K == kProduct) {
+        int tiles;
+        RowTile t;
+        row_tile(job.ends, job.experts, job.rows, TN, -1, &t, &tiles);
+        tiles = uniform(tiles);
+        if (blockIdx.x >= across * tiles) return;
+        grid_tile(in_order(blockIdx.x, across * tiles), across, tiles, tm, tn);
+        row_tile(job.ends, job.experts, job.rows, TN, uniform((int)tn), &t);  // there is one
+        expert = uniform(t.expert);
+        inner0 = (int64_t)uniform((int)tm) * TM;
+        outer0 = uniform(t.first);
+        outer_end = uniform(t.end);
+        reduce = job.kbytes;
+        if (expert < 0) {
+            for (int i = tid; i < TM * TN; i += 64 * W)
+                if (outer0 + i / TM < outer_end && inner0 + i % TM < job.inner)
+                    out[(outer0 + i / TM) * job.ldo + inner0 + i % TM] = TO(0);
+            return;
+        }
+        a += expert * job.astride + (AT ? inner0 * T::kSize : inner0 * job.lda);
+        b += outer0 * job.ldb;
+    } else {
+        // expert after expert, each spread over all XCDs: they may have very different numbers of rows
+        const int64_t down = (job.outer + TN - 1) / TN, per = across * down;
+        expert = (int)(blockIdx.x / per);
+        grid_tile(in_order(blockIdx.x % per, per), across, down, tm, tn);
+        inner0 = (int64_t)uniform((int)tm) * TM;
+        outer0 = (int64_t)uniform((int)tn) * TN;
+        outer_end = job.outer;
+        expert = uniform(expert);
+        const int first = uniform(expert == 0 ? 0 : end_of(job.ends, expert - 1, job.rows));
+        reduce = (int64_t)uniform(max(end_of(job.ends, expert, job.rows) - first, 0)) * T::kSize;
+        a += first * job.lda + inner0 * T::kSize;
+        b += first * job.ldb + outer0 * T::kSize;
+        out += expert * job.ostride;
+    }
+    const int full = (int)(reduce / 64), steps = 2 * (int)((reduce + 127) / 128);
+    LoadsA la;
+    LoadsB lb;
+    la.init(a, job.lda, (int)min(job.inner - inner0, (int64_t)TM), wave, lane);
+    lb.init(b, job.ldb, (int)min(outer_end - outer0, (int64_t)TN), wave, lane);
+
+    typename T::Sum acc[TA][2][TB][2];  // pairs of 16: tiles of 32 x 32
+#pragma unroll
+    for (int i = 0; i < 2 * TA; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * TB; ++j) acc[i >> 1][i & 1][j >> 1][j & 1] = typename T::Sum{0, 0, 0, 0};
+
+    // load number j of step t into its buffer (behind the last step: the last step again, into a
+    // buffer that nobody reads any more)
+    constexpr int kLoads = LoadsA::kCount + LoadsB::kCount, kLate = TA > 1 ? kLoads / 2 : 0;
+    auto load = [&](auto end, int j, int t, Buffer& buf) __attribute__((always_inline)) {
+        const int s = !end.value || t < steps ? t : steps - 1;
+        if (!end.value || s < full) {
+            if (j < LoadsA::kCount) la.load(j, s, buf.a, wave);
+            else lb.load(j - LoadsA::kCount, s, buf.b, wave);
+        } else {
+            if (j < LoadsA::kCount) la.load_end(j, s, reduce, buf.a, wave, lane);
+            else lb.load_end(j - LoadsA::kCount, s, reduce, buf.b, wave, lane);
+        }
+    };
+    u32x4 fa[2][2], fb[2][TB][2];
+    auto read_a = [&](int i, const Buffer& buf) __attribute__((always_inline)) {  // 32 columns into the set i & 1
+#pragma unroll
+        for (int p = 0; p < 2; ++p) fa[i & 1][p] = LoadsA::fragment(buf.a, (TM / WM) * wm + 32 * i + 16 * p, lane);
+    };
+    auto read_b = [&](int set, const Buffer& buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                fb[set][j][p] = LoadsB::fragment(buf.b, (TN / WN) * wn + 32 * j + 16 * p, lane);
+    };
+    // Step t, whose first operands are in registers (set t & 1).  The loads of step t + R - 1 go
+    // out after the barrier, the last kLate of them in the first half of the next step.
+    auto step = [&](auto end, int t, int set, const Buffer& buf, const Buffer& next, Buffer& early,
+                    Buffer& late) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < TA; ++i) {
+            if (i == TA / 2) {
+                // the next step's loads have landed, and every wave is past the step before
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 3) * kLoads) : "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (i + 1 < TA) {
+                read_a(i + 1, buf);
+            } else {
+                read_b(set ^ 1, next);
+                if (TA > 1) read_a(0, next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    acc[i][p >> 1][j][p & 1] = T::mma(fa[i & 1][p >> 1], fb[set][j][p & 1], acc[i][p >> 1][j][p & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+                constexpr int kSlots = TA > 1 ? TA / 2 * TB : TB;  // of a half step
+                const int slot = (i >= TA / 2 ? i - TA / 2 : i) * TB + j;
+                if (i >= TA / 2) {
+#pragma unroll
+                    for (int l = slot; l < kLoads - kLate; l += kSlots) load(end, l, t + R - 1, early);
+                } else {
+#pragma unroll
+                    for (int l = slot; l < kLate; l += kSlots) load(end, kLoads - kLate + l, t + R - 2, late);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (TA == 1) read_a(0, next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if (steps > 0) {
+#pragma unroll
+        for (int t = 0; t < R - 1; ++t)
+#pragma unroll
+            for (int j = 0; j < (t == R - 2 ? kLoads - kLate : kLoads); ++j) load(AtEnd(), j, t, ring[t]);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 2) * kLoads - kLate) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read_b(0, ring[0]);
+        read_a(0, ring[0]);
+        const auto inc = [](int v) { return v == R - 1 ? 0 : v + 1; };
+        const auto dec = [](int v) { return v == 0 ? R - 1 : v - 1; };
+        int cur = 0, t = 0;
+        const auto two_steps = [&](auto end) __attribute__((always_inline)) {
+            const int one = inc(cur), two = inc(one), last = dec(cur);
+            step(end, t, 0, ring[cur], ring[one], ring[last], ring[dec(last)]);
+            step(end, t + 1, 1, ring[one], ring[two], ring[cur], ring[last]);
+            cur = two;
+        };
+        for (; t + R < full; t += 2) two_steps(Inside());
+        for (; t < steps; t += 2) two_steps(AtEnd());
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * TB; ++j) {
+        const int64_t row = outer0 + (TN / WN) * wn + 16 * j + (lane & 15);
+        if (row >= outer_end) continue;
+#pragma unroll
+        for (int i = 0; i < 2 * TA; ++i)
+            finish<T, K>(job, expert, row, inner0 + (TM / WM) * wm + 16 * i + 4 * (lane >> 4),
+                         acc[i >> 1][i & 1][j >> 1][j & 1], out + row * job.ldo);
+    }
+}
+
 template <class T, bool AT, bool BT, Kind K, class TO>
 int any(const GroupedJob& job, void* stream) {
     const int64_t across = (job.inner + 63) / 64;
@@ -311,26 +582,71 @@ int few(const GroupedJob& job, void* stream) {
     return (int)hipGetLastError();
 }
 
+// Direct loads take 16 bytes of an aligned row at a time.
+bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0 && ld < kMaxRow;
+}
+
+template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, class TO>
+int tile(const GroupedJob& job, void* stream) {
+    const int64_t across = (job.inner + TM - 1) / TM;
+    const int64_t down = K == kGradient ? (job.outer + TN - 1) / TN * job.experts
+                                        : most_row_tiles(job.rows, job.experts, TN, job.ends != nullptr);
+    if (across > (int64_t)0xFFFFFFFF / (64 * WM * WN) / down) return kGridTooLarge;
+    hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, TO>), dim3((unsigned)(across * down)),
+                       dim3(64 * WM * WN), 0, (hipStream_t)stream, job);
+    return (int)hipGetLastError();
+}
+
+// The largest tile that leaves every CU a workgroup, counting half a tile more for each expert:
+// 0: 256 x 256, 1: 128 x 64, 2: 64 x 64.  Measured (us) for 0 / 1 / 2: 16384 rows of 8 experts 11008 x
+// 4096: 1395 / 2568 / 3217; 1003 rows of 16 experts 2048 x 4096: 100 / 88 / 89; 200 rows of them: 86 / 65 /
+// 65; weight gradients, 8192 rows of 16 experts 2048 x 4096: 237 / 306 / 351; 1001 rows of 4 1024 x 1024: 22 /
+// 11 / 11.
+template <Kind K>
+int pick_tile(const GroupedJob& job) {
+    const auto tiles = [&](int64_t m, int64_t n) {
+        const int64_t across = (job.inner + m - 1) / m;
+        return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
+                                        : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts / 2 : 0));
+    };
+    return tiles(256, 256) >= 256 ? 0 : tiles(128, 64) >= 256 ? 1 : 2;
+}
+
+template <class T, bool AT, bool BT, Kind K, class TO>
+int product(const GroupedJob& job, void* stream) {
+    const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
+    const bool ok = direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) &&
+                    direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes);
+    if (!ok) return any<T, AT, BT, K, TO>(job, stream);
+    const int variant = pick_tile<K>(job);
+    switch (variant) {
+        case 0: return tile<T, AT, BT, K, 256, 256, 2, 4, 4, TO>(job, stream);
+        case 1: return tile<T, AT, BT, K, 128, 64, 2, 2, 4, TO>(job, stream);
+        default: return tile<T, AT, BT, K, 64, 64, 2, 2, 4, TO>(job, stream);
+    }
+}
+
 }  // namespace
 
 int launch_grouped_mm(const GroupedJob& job, bool transposed, bool bf16out, void* stream) {
     if (transposed)
-        return bf16out ? any<Bf16, true, false, kProduct, uint16_t>(job, stream)
-                       : any<Bf16, true, false, kProduct, float>(job, stream);
-    return bf16out ? any<Bf16, false, false, kProduct, uint16_t>(job, stream)
-                   : any<Bf16, false, false, kProduct, float>(job, stream);
+        return bf16out ? product<Bf16, true, false, kProduct, uint16_t>(job, stream)
+                       : product<Bf16, true, false, kProduct, float>(job, stream);
+    return bf16out ? product<Bf16, false, false, kProduct, uint16_t>(job, stream)
+                   : product<Bf16, false, false, kProduct, float>(job, stream);
 }
 
 int launch_grouped_wgrad(const GroupedJob& job, bool bf16out, void* stream) {
-    return bf16out ? any<Bf16, true, true, kGradient, uint16_t>(job, stream)
-                   : any<Bf16, true, true, kGradient, float>(job, stream);
+    return bf16out ? product<Bf16, true, true, kGradient, uint16_t>(job, stream)
+                   : product<Bf16, true, true, kGradient, float>(job, stream);
 }
 
 int launch_gemm_int8(const GroupedJob& job, bool bf16x, bool bf16out, void* stream) {
     if (bf16x)
         return bf16out ? few<Int8, true, 1, 1, uint16_t>(job, stream) : few<Int8, true, 1, 1, float>(job, stream);
-    return bf16out ? any<Int8, false, false, kProduct, uint16_t>(job, stream)
-                   : any<Int8, false, false, kProduct, float>(job, stream);
+    return bf16out ? product<Int8, false, false, kProduct, uint16_t>(job, stream)
+                   : product<Int8, false, false, kProduct, float>(job, stream);
 }
 
 }  // namespace tsenor

@@ -14,19 +14,14 @@ using namespace fp8;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-// One matrix instruction takes 16 bytes of the reduction from each lane half h = lane / 32:
-// A row lane % 32, B column lane % 32; result column lane % 32, rows 8 i0 + 4 h + i1 in
-// register 4 i0 + i1.  32 bytes of a row in all: 16 bf16 or 32 integers.
+// One matrix instruction takes 64 bytes of the reduction (32 bf16 or 64 integers), 16 from each
+// lane quarter q = lane / 16: A row lane % 16, B column lane % 16; result column lane % 16, rows
+// 4 q .. 4 q + 3.  The 32 x 32 instructions, at the same rate, read and write twice as many bytes
+// of sums for a product; under the card's power limit that costs clock.
 struct Bf16 {
     static constexpr int kSize = 2;
-    typedef f32x16 Sum;
-    typedef f32x4 Sum4;
-    __device__ static __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
-                                                       c, 0, 0, 0);
-    }
+    typedef f32x4 Sum;
     __device__ static __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
@@ -34,12 +29,7 @@ struct Bf16 {
 };
 struct Int8 {
     static constexpr int kSize = 1;
-    typedef i32x16 Sum;
-    typedef i32x4 Sum4;
-    __device__ static __forceinline__ i32x16 mma(u32x4 a, u32x4 b, i32x16 c) {
-        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
-                                                     0, 0, 0);
-    }
+    typedef i32x4 Sum;
     __device__ static __forceinline__ i32x4 mma(u32x4 a, u32x4 b, i32x4 c) {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c,
                                                      0, 0, 0);
@@ -48,35 +38,42 @@ struct Int8 {
 
 // LDS tiles of one step, 64 bytes of the reduction for `W` rows or columns, in chunks of 16
 // bytes.  An operand that is contiguous along the reduction is kept by rows of 64 bytes, chunk c of
-// row r at c ^ ((r >> 2) & 3): the 16 rows of one pass of a 16-byte read then hit different
-// banks.  One that is contiguous along its columns (bf16) is kept as it lies, 32 rows of the
-// reduction of W entries, and turned by the transposing read below; pairs of chunks are moved
-// so that the four rows of such a read hit different banks.
-__device__ __forceinline__ int row_slot(int r, int c) { return 4 * r + (c ^ ((r >> 2) & 3)); }
+// row r at c ^ (-(r / 4) & 3).  A 16-byte read serves lanes 0-3, 12-15, 20-23 and 24-27 at once, then
+// 4-11, 16-19 and 28-31, and so on (measured: c ^ (r / 4 & 3) conflicts); with lane % 16 the row and
+// lane / 16 the chunk, these lie in different banks.  One that is contiguous along its columns
+// (bf16) is kept as it lies, 32 rows of the reduction of W entries, and turned by the transposing
+// read below; pairs of chunks are moved so that the eight rows of half such a read hit different banks.
+__device__ __forceinline__ int row_slot(int r, int c) { return 4 * r + (c ^ (-(r >> 2) & 3)); }
 template <int W>
 __device__ __forceinline__ int turned_slot(int r, int c) {  // chunk c of reduction row r
     constexpr int kChunks = W / 8;
-    const int f = W >= 128 ? 4 * (r & 3) : 4 * ((r >> 1) & 1);
-    return kChunks * r + (c ^ f);
+    const int f = W >= 128 ? (r & 3) | ((r >> 1) & 4) : ((r >> 1) & 1) | ((r >> 2) & 2);
+    return kChunks * r + (c ^ (2 * f));
 }
 
-// Fragment kc (0, 1) of rows row0 .. row0 + 31: chunk 2 kc + h of row lane % 32.
-__device__ __forceinline__ u32x4 row_fragment(const u32x4* tile, int row0, int kc, int lane) {
-    return tile[row_slot(row0 + (lane & 31), 2 * kc + (lane >> 5))];
+// Rows row0 .. row0 + 15: chunk q of row lane % 16.
+__device__ __forceinline__ u32x4 row_fragment(const u32x4* tile, int row0, int lane) {
+    return tile[row_slot(row0 + (lane & 15), lane >> 4)];
 }
 // The same of a column-contiguous tile.  ds_read_b64_tr_b16, for each 16 lanes: lane i gives the
 // address of 4 entries, of row i / 4 and columns 4 (i % 4) ..; it receives column i of the four
 // rows (probed).  Two such reads give a lane the eight reduction entries of its column.
 template <int W>
-__device__ __forceinline__ u32x4 turned_fragment(const u32x4* tile, int col0, int kc, int lane) {
+__device__ __forceinline__ u32x4 turned_fragment(const u32x4* tile, int col0, int lane) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const int g = lane >> 4, i = lane & 15;
-    const int row = 16 * kc + 8 * (g >> 1) + (i >> 2), chunk = (col0 >> 3) + 2 * (g & 1) + ((i & 3) >> 1);
+    const int i = lane & 15, row = 8 * (lane >> 4) + (i >> 2), chunk = (col0 >> 3) + ((i & 3) >> 1);
     const uint8_t* base = reinterpret_cast<const uint8_t*>(tile) + 8 * (i & 1);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + 16 * turned_slot<W>(row, chunk)));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + 16 * turned_slot<W>(row + 4, chunk)));
     const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
     return u32x4{a.x, a.y, b.x, b.y};
+}
+
+// A value that all lanes have, as the compiler has to know it for scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+    const u32x2 v = __builtin_bit_cast(u32x2, p);
+    return __builtin_bit_cast(const uint8_t*, u32x2{(uint32_t)uniform((int)v.x), (uint32_t)uniform((int)v.y)});
 }
 
 // Where the rows of one tile lie.
