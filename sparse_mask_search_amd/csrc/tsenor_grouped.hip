@@ -312,6 +312,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
 // would stall every wave on the address unit.  Rows and columns behind an operand's end
 // repeat its last one (nothing of them is stored); behind the reduction's end zeros are loaded.
 
+constexpr int64_t kCus = 256;
 constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside a tile fit 32 bits
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
@@ -349,12 +350,14 @@ struct Loads {
             }
         }
     }
-    __device__ __forceinline__ void load(int j, int64_t s, const u32x4* tile, int wave) const {
-        dma16(base + s * step, offset[j], lds_offset(tile + 64 * (wave * kCount + j)));
-    }
-    // the same with zeros behind the reduction's `reduce` bytes (turned: of one column)
-    __device__ __forceinline__ void load_end(int j, int64_t s, int64_t reduce, const u32x4* tile, int wave,
-                                             int lane) const {
+    // Step s; not inside: with zeros behind the reduction's `reduce` bytes (turned: of one column).
+    __device__ static __forceinline__ void load(const Loads& of, bool inside, int j, int64_t s, int64_t reduce,
+                                                const u32x4* tile, int wave, int lane) {
+        const uint32_t to = lds_offset(tile + 64 * (wave * kCount + j));
+        if (inside) {
+            dma16(of.base + s * of.step, of.offset[j], to);
+            return;
+        }
         const int slot = 64 * (wave * kCount + j) + lane;
         int64_t at;
         if constexpr (TURNED) {
@@ -363,14 +366,85 @@ struct Loads {
             const int r = slot / 4;
             at = 64 * s + 16 * (row_slot(r, slot % 4) - 4 * r);
         }
-        const uint8_t* p = at < reduce ? base + s * step + offset[j] : reinterpret_cast<const uint8_t*>(&kZeros);
-        dma16_at(p, lds_offset(tile + 64 * (wave * kCount + j)));
+        const uint8_t* p = at < reduce ? of.base + s * of.step + of.offset[j] : reinterpret_cast<const uint8_t*>(&kZeros);
+        dma16_at(p, to);
     }
     __device__ static __forceinline__ u32x4 fragment(const u32x4* tile, int at, int lane) {
         if constexpr (TURNED) return turned_fragment<S>(tile, at, lane);
         else return row_fragment(tile, at, lane);
     }
 };
+
+// The results of a wave's FA x FB tiles of 16 x 16, rows row0 + STEP j, columns c0 + 16 i + 4 q (c0 a
+// multiple of 32).  Whole tiles: what scales or masks them is loaded first (a load among the
+// stores would wait for all of those before it), and bf16 results of two neighbouring tiles change
+// places between the lane quarters, so that a store has 16 bytes.
+template <class T, Kind K, int FA, int FB, int STEP, class TO>
+__device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, int row0, int rows, int c0, int q,
+                                           const typename T::Sum* sums, TO* out) {
+    constexpr bool kScaled = T::kSize == 1, kMasked = K == kGradient, kHalf = sizeof(TO) == 2;
+    if (c0 + 16 * FA > (int)job.inner || !(kHalf ? job.ovec8 : job.ovec)) {
+#pragma unroll
+        for (int j = 0; j < FB; ++j) {
+            const int row = row0 + STEP * j;
+            if (row >= rows) continue;
+#pragma unroll
+            for (int i = 0; i < FA; ++i)
+                finish<T, K>(job, expert, row, c0 + 16 * i + 4 * q, sums[i * FB + j], out + row * job.ldo);
+        }
+        return;
+    }
+    f32x4 across[kScaled ? FA : 1];
+    float down[kScaled ? FB : 1];
+    uint32_t keep[kMasked ? FB : 1][kMasked ? FA / 2 : 1];
+    if constexpr (kScaled) {
+        const float* as = job.as + expert * job.inner + c0 + 4 * q;
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) across[i][e] = as[16 * i + e];
+#pragma unroll
+        for (int j = 0; j < FB; ++j) down[j] = job.bs[min(row0 + STEP * j, rows - 1)];
+    }
+    if constexpr (kMasked) {
+        const int64_t words = (job.inner + 31) / 32;
+#pragma unroll
+        for (int j = 0; j < FB; ++j) {
+            const uint32_t* row = job.mask + (expert * job.outer + min(row0 + STEP * j, rows - 1)) * words + (c0 >> 5);
+#pragma unroll
+            for (int i = 0; i < FA / 2; ++i) keep[j][i] = job.mask == nullptr ? 0xFFFFFFFFu : row[i];
+        }
+    }
+    TO* y = out + row0 * job.ldo + c0 + (kHalf ? 16 * (q & 1) + 8 * (q >> 1) : 4 * q);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+#pragma unroll
+        for (int i = 0; i < FA; i += 2) {
+            __builtin_amdgcn_sched_barrier(0);  // or results of several stores are made at once, and spilled
+            f32x4 v[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = (float)sums[(i + p) * FB + j][e];
+                    if constexpr (kScaled) x = x * down[j] * across[i + p][e];
+                    if constexpr (kMasked) x = (keep[j][i / 2] >> (16 * p + 4 * q + e)) & 1u ? x : 0.f;
+                    v[p][e] = x;
+                }
+            if constexpr (kHalf) {
+                const u32x2 lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][0], v[0][1]),
+                                                                  pack_bf16(v[1][0], v[1][1]), false, false);
+                const u32x2 hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][2], v[0][3]),
+                                                                  pack_bf16(v[1][2], v[1][3]), false, false);
+                if (row0 + STEP * j < rows) *reinterpret_cast<u32x4*>(y + 16 * i) = u32x4{lo.x, hi.x, lo.y, hi.y};
+            } else if (row0 + STEP * j < rows) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) *reinterpret_cast<f32x4*>(y + 16 * (i + p)) = v[p];
+            }
+        }
+        y += STEP * job.ldo;
+    }
+}
 
 // Work t of `count` for workgroup `bid`: workgroups go to the chip's 8 XCDs round robin and each
 // XCD has its own L2, so XCD x gets a contiguous range.
@@ -393,103 +467,132 @@ struct Inside {
 struct AtEnd {
     static constexpr bool value = true;
 };
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
 
-template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, class TO>
+template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, class TO>
 __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const GroupedJob job) {
     constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
     typedef Loads<T, AT, TM, W> LoadsA;
     typedef Loads<T, BT, TN, W> LoadsB;
-    static_assert(R >= 3, "ring");
+    static_assert(R == 4, "a tile has at least R steps");
     struct Buffer {
         u32x4 a[TM * 4];
         u32x4 b[TN * 4];
     };
     __shared__ Buffer ring[R];
+    __shared__ int table[LONG ? 2 * (kMaxExperts + 1) : 1];  // first tile and first row of each expert
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int64_t across = (job.inner + TM - 1) / TM;
-    const uint8_t *a = static_cast<const uint8_t*>(job.a), *b = static_cast<const uint8_t*>(job.b);
-    TO* out = static_cast<TO*>(job.out);
-    int64_t inner0, outer0, outer_end, reduce, tm, tn;
-    int expert;
+    const int across = (int)((job.inner + TM - 1) / TM);
+    const int down = K == kGradient ? (int)((job.outer + TN - 1) / TN) : 0;  // of one expert
+
+    struct Tile {  // the same in all lanes, but for the loads' offsets
+        int expert, inner0, outer0, outer_end, full, steps;
+        int64_t reduce;
+        LoadsA la;
+        LoadsB lb;
+    };
+    int64_t total, work = blockIdx.x;  // tiles of the launch; this workgroup's next one
     if constexpr (K == kProduct) {
         int tiles;
-        RowTile t;
-        row_tile(job.ends, job.experts, job.rows, TN, -1, &t, &tiles);
-        tiles = uniform(tiles);
-        if (blockIdx.x >= across * tiles) return;
-        grid_tile(in_order(blockIdx.x, across * tiles), across, tiles, tm, tn);
-        row_tile(job.ends, job.experts, job.rows, TN, uniform((int)tn), &t);  // there is one
-        expert = uniform(t.expert);
-        inner0 = (int64_t)uniform((int)tm) * TM;
-        outer0 = uniform(t.first);
-        outer_end = uniform(t.end);
-        reduce = job.kbytes;
-        if (expert < 0) {
-            for (int i = tid; i < TM * TN; i += 64 * W)
-                if (outer0 + i / TM < outer_end && inner0 + i % TM < job.inner)
-                    out[(outer0 + i / TM) * job.ldo + inner0 + i % TM] = TO(0);
-            return;
-        }
-        a += expert * job.astride + (AT ? inner0 * T::kSize : inner0 * job.lda);
-        b += outer0 * job.ldb;
-    } else {
-        // expert after expert, each spread over all XCDs: they may have very different numbers of rows
-        const int64_t down = (job.outer + TN - 1) / TN, per = across * down;
-        expert = (int)(blockIdx.x / per);
-        grid_tile(in_order(blockIdx.x % per, per), across, down, tm, tn);
-        inner0 = (int64_t)uniform((int)tm) * TM;
-        outer0 = (int64_t)uniform((int)tn) * TN;
-        outer_end = job.outer;
-        expert = uniform(expert);
-        const int first = uniform(expert == 0 ? 0 : end_of(job.ends, expert - 1, job.rows));
-        reduce = (int64_t)uniform(max(end_of(job.ends, expert, job.rows) - first, 0)) * T::kSize;
-        a += first * job.lda + inner0 * T::kSize;
-        b += first * job.ldb + outer0 * T::kSize;
-        out += expert * job.ostride;
-    }
-    const int full = (int)(reduce / 64), steps = 2 * (int)((reduce + 127) / 128);
-    LoadsA la;
-    LoadsB lb;
-    la.init(a, job.lda, (int)min(job.inner - inner0, (int64_t)TM), wave, lane);
-    lb.init(b, job.ldb, (int)min(outer_end - outer0, (int64_t)TN), wave, lane);
-
-    typename T::Sum acc[TA][2][TB][2];  // pairs of 16: tiles of 32 x 32
-#pragma unroll
-    for (int i = 0; i < 2 * TA; ++i)
-#pragma unroll
-        for (int j = 0; j < 2 * TB; ++j) acc[i >> 1][i & 1][j >> 1][j & 1] = typename T::Sum{0, 0, 0, 0};
-
-    // load number j of step t into its buffer (behind the last step: the last step again, into a
-    // buffer that nobody reads any more)
-    constexpr int kLoads = LoadsA::kCount + LoadsB::kCount, kLate = TA > 1 ? kLoads / 2 : 0;
-    auto load = [&](auto end, int j, int t, Buffer& buf) __attribute__((always_inline)) {
-        const int s = !end.value || t < steps ? t : steps - 1;
-        if (!end.value || s < full) {
-            if (j < LoadsA::kCount) la.load(j, s, buf.a, wave);
-            else lb.load(j - LoadsA::kCount, s, buf.b, wave);
+        RowTile none;
+        if constexpr (LONG) {
+            tiles = row_table(job.ends, job.experts, job.rows, TN, table);
+            __syncthreads();
         } else {
-            if (j < LoadsA::kCount) la.load_end(j, s, reduce, buf.a, wave, lane);
-            else lb.load_end(j - LoadsA::kCount, s, reduce, buf.b, wave, lane);
+            row_tile(job.ends, job.experts, job.rows, TN, -1, &none, &tiles);
         }
+        total = (int64_t)across * uniform(tiles);
+    } else {
+        total = (int64_t)across * down * job.experts;
+    }
+    // The next tile that has something to add up; the others' results are zeros, written here.
+    const auto find = [&](Tile& to) __attribute__((always_inline)) {
+        for (; work < total; work += LONG ? (int64_t)gridDim.x : total) {
+            const uint8_t *a = static_cast<const uint8_t*>(job.a), *b = static_cast<const uint8_t*>(job.b);
+            int64_t tm, tn;
+            if constexpr (K == kProduct) {
+                RowTile t;
+                grid_tile(in_order(work, total), across, total / across, tm, tn);
+                if constexpr (LONG) t = row_tile_of(table, job.experts, job.rows, TN, uniform((int)tn));
+                else row_tile(job.ends, job.experts, job.rows, TN, uniform((int)tn), &t);
+                to.expert = uniform(t.expert);
+                to.inner0 = uniform((int)tm) * TM;
+                to.outer0 = uniform(t.first);
+                to.outer_end = uniform(t.end);
+                to.reduce = to.expert < 0 ? 0 : job.kbytes;
+                a += to.expert * job.astride + (AT ? (int64_t)to.inner0 * T::kSize : to.inner0 * job.lda);
+                b += to.outer0 * job.ldb;
+            } else {
+                // expert after expert, each spread over all XCDs: they may have very different numbers of rows
+                const int64_t per = (int64_t)across * down;
+                to.expert = uniform((int)(work / per));
+                grid_tile(in_order(work % per, per), across, down, tm, tn);
+                to.inner0 = uniform((int)tm) * TM;
+                to.outer0 = uniform((int)tn) * TN;
+                to.outer_end = (int)job.outer;
+                const int first = uniform(to.expert == 0 ? 0 : end_of(job.ends, to.expert - 1, job.rows));
+                to.reduce = (int64_t)uniform(max(end_of(job.ends, to.expert, job.rows) - first, 0)) * T::kSize;
+                a += first * job.lda + (int64_t)to.inner0 * T::kSize;
+                b += first * job.ldb + (int64_t)to.outer0 * T::kSize;
+            }
+            if (to.reduce == 0) {
+                TO* out = static_cast<TO*>(job.out) + (K == kGradient ? to.expert * job.ostride : 0);
+                for (int i = tid; i < TM * TN; i += 64 * W)
+                    if (to.outer0 + i / TM < to.outer_end && to.inner0 + i % TM < job.inner)
+                        out[(to.outer0 + (int64_t)(i / TM)) * job.ldo + to.inner0 + i % TM] = TO(0);
+                continue;
+            }
+            to.full = (int)(to.reduce / 64);
+            to.steps = max(2 * (int)((to.reduce + 127) / 128), R);
+            to.la.init(a, job.lda, (int)min(job.inner - to.inner0, (int64_t)TM), wave, lane);
+            to.lb.init(b, job.ldb, min(to.outer_end - to.outer0, TN), wave, lane);
+            work += LONG ? (int64_t)gridDim.x : total;
+            return true;
+        }
+        return false;
     };
+    Tile cur, nxt;
+    if (!find(cur)) return;
+    nxt = cur;
+    nxt.full = 0;
+    nxt.reduce = 0;  // nothing: zeros are loaded
+
+    // Load number j of the tile's step t into its buffer; steps behind the last are the next tile's first
+    // ones, so that they are on their way while this tile's results are written.
+    constexpr int kLoads = LoadsA::kCount + LoadsB::kCount, kLate = TA > 1 ? kLoads / 2 : 0;
+    const auto load = [&](auto end, int j, int t, Buffer& buf) __attribute__((always_inline)) {
+        const bool ahead = end.value && t >= cur.steps;
+        const int s = ahead ? t - cur.steps : t;
+        const bool inside = !end.value || s < (ahead ? nxt.full : cur.full);
+        if (j < LoadsA::kCount)
+            LoadsA::load(ahead ? nxt.la : cur.la, inside, j, s, ahead ? nxt.reduce : cur.reduce, buf.a, wave, lane);
+        else
+            LoadsB::load(ahead ? nxt.lb : cur.lb, inside, j - LoadsA::kCount, s, ahead ? nxt.reduce : cur.reduce, buf.b,
+                         wave, lane);
+    };
+    typename T::Sum acc[TA][2][TB][2];  // pairs of 16: tiles of 32 x 32
     u32x4 fa[2][2], fb[2][TB][2];
-    auto read_a = [&](int i, const Buffer& buf) __attribute__((always_inline)) {  // 32 columns into the set i & 1
+    const auto read_a = [&](int i, const Buffer& buf) __attribute__((always_inline)) {  // into the set i & 1
 #pragma unroll
         for (int p = 0; p < 2; ++p) fa[i & 1][p] = LoadsA::fragment(buf.a, (TM / WM) * wm + 32 * i + 16 * p, lane);
     };
-    auto read_b = [&](int set, const Buffer& buf) __attribute__((always_inline)) {
+    // (a wave's rows lie WN fragments apart, so that all waves share what a short tile has)
+    const auto read_b = [&](auto pairs, int set, const Buffer& buf) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TB; ++j)
+        for (int j = 0; j < pairs.value; ++j)
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-                fb[set][j][p] = LoadsB::fragment(buf.b, (TN / WN) * wn + 32 * j + 16 * p, lane);
+                fb[set][j][p] = LoadsB::fragment(buf.b, 16 * (WN * (2 * j + p) + wn), lane);
     };
     // Step t, whose first operands are in registers (set t & 1).  The loads of step t + R - 1 go
     // out after the barrier, the last kLate of them in the first half of the next step.
-    auto step = [&](auto end, int t, int set, const Buffer& buf, const Buffer& next, Buffer& early,
-                    Buffer& late) __attribute__((always_inline)) {
+    const auto step = [&](auto end, auto pairs, int t, int set, const Buffer& buf, const Buffer& next, Buffer& early,
+                          Buffer& late) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < TA; ++i) {
             if (i == TA / 2) {
@@ -502,18 +605,19 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             if (i + 1 < TA) {
                 read_a(i + 1, buf);
             } else {
-                read_b(set ^ 1, next);
+                if constexpr (end.value) read_b(Count<TB>(), set ^ 1, next);
+                else read_b(pairs, set ^ 1, next);
                 if (TA > 1) read_a(0, next);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < TB; ++j) {
+            for (int j = 0; j < pairs.value; ++j) {
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
                     acc[i][p >> 1][j][p & 1] = T::mma(fa[i & 1][p >> 1], fb[set][j][p & 1], acc[i][p >> 1][j][p & 1]);
                 __builtin_amdgcn_sched_barrier(0);
-                constexpr int kSlots = TA > 1 ? TA / 2 * TB : TB;  // of a half step
-                const int slot = (i >= TA / 2 ? i - TA / 2 : i) * TB + j;
+                constexpr int kSlots = TA > 1 ? TA / 2 * pairs.value : pairs.value;  // of a half step
+                const int slot = (i >= TA / 2 ? i - TA / 2 : i) * pairs.value + j;
                 if (i >= TA / 2) {
 #pragma unroll
                     for (int l = slot; l < kLoads - kLate; l += kSlots) load(end, l, t + R - 1, early);
@@ -527,38 +631,51 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if (steps > 0) {
 #pragma unroll
-        for (int t = 0; t < R - 1; ++t)
+    for (int t = 0; t < R - 1; ++t)
 #pragma unroll
-            for (int j = 0; j < (t == R - 2 ? kLoads - kLate : kLoads); ++j) load(AtEnd(), j, t, ring[t]);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 2) * kLoads - kLate) : "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        read_b(0, ring[0]);
-        read_a(0, ring[0]);
-        const auto inc = [](int v) { return v == R - 1 ? 0 : v + 1; };
-        const auto dec = [](int v) { return v == 0 ? R - 1 : v - 1; };
-        int cur = 0, t = 0;
-        const auto two_steps = [&](auto end) __attribute__((always_inline)) {
-            const int one = inc(cur), two = inc(one), last = dec(cur);
-            step(end, t, 0, ring[cur], ring[one], ring[last], ring[dec(last)]);
-            step(end, t + 1, 1, ring[one], ring[two], ring[cur], ring[last]);
-            cur = two;
-        };
-        for (; t + R < full; t += 2) two_steps(Inside());
-        for (; t < steps; t += 2) two_steps(AtEnd());
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    }
-#pragma unroll
-    for (int j = 0; j < 2 * TB; ++j) {
-        const int64_t row = outer0 + (TN / WN) * wn + 16 * j + (lane & 15);
-        if (row >= outer_end) continue;
+        for (int j = 0; j < (t == R - 2 ? kLoads - kLate : kLoads); ++j) load(AtEnd(), j, t, ring[t]);
+    bool more = false;
+    if constexpr (LONG) more = find(nxt);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 2) * kLoads - kLate) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_b(Count<TB>(), 0, ring[0]);
+    read_a(0, ring[0]);
+    const auto inc = [](int v) { return v == R - 1 ? 0 : v + 1; };
+    const auto dec = [](int v) { return v == 0 ? R - 1 : v - 1; };
+    int at = 0;  // the buffer of the current step
+    for (;;) {
 #pragma unroll
         for (int i = 0; i < 2 * TA; ++i)
-            finish<T, K>(job, expert, row, inner0 + (TM / WM) * wm + 16 * i + 4 * (lane >> 4),
-                         acc[i >> 1][i & 1][j >> 1][j & 1], out + row * job.ldo);
+#pragma unroll
+            for (int j = 0; j < 2 * TB; ++j) acc[i >> 1][i & 1][j >> 1][j & 1] = typename T::Sum{0, 0, 0, 0};
+        int t = 0;
+        const auto two_steps = [&](auto end, auto pairs) __attribute__((always_inline)) {
+            const int one = inc(at), two = inc(one), last = dec(at);
+            step(end, pairs, t, 0, ring[at], ring[one], ring[last], ring[dec(last)]);
+            step(end, pairs, t + 1, 1, ring[one], ring[two], ring[at], ring[last]);
+            at = two;
+        };
+        const auto all_steps = [&](auto pairs) __attribute__((always_inline)) {
+            for (; t + R < cur.full; t += 2) two_steps(Inside(), pairs);
+            for (; t < cur.steps; t += 2) two_steps(AtEnd(), pairs);
+        };
+        // an expert's last rows fill half a tile at most as often as not
+        if (K == kProduct && TB > 1 && cur.outer_end - cur.outer0 <= TN / 2) all_steps(Count<TB / 2 + (TB == 1)>());
+        else all_steps(Count<TB>());
+        const int row0 = cur.outer0 + 16 * wn + (lane & 15), c0 = cur.inner0 + (TM / WM) * wm;
+        store_tile<T, K, 2 * TA, 2 * TB, 16 * WN>(job, cur.expert, row0, cur.outer_end, c0, lane >> 4, &acc[0][0][0][0],
+                                         static_cast<TO*>(job.out) + (K == kGradient ? cur.expert * job.ostride : 0));
+        if (!more) break;
+        cur = nxt;
+        more = find(nxt);
+        if (!more) {
+            nxt.full = 0;
+            nxt.reduce = 0;
+        }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <class T, bool AT, bool BT, Kind K, class TO>
@@ -587,13 +704,14 @@ bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0 && ld < kMaxRow;
 }
 
-template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, class TO>
+template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, class TO>
 int tile(const GroupedJob& job, void* stream) {
     const int64_t across = (job.inner + TM - 1) / TM;
     const int64_t down = K == kGradient ? (job.outer + TN - 1) / TN * job.experts
                                         : most_row_tiles(job.rows, job.experts, TN, job.ends != nullptr);
     if (across > (int64_t)0xFFFFFFFF / (64 * WM * WN) / down) return kGridTooLarge;
-    hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, TO>), dim3((unsigned)(across * down)),
+    const int64_t groups = LONG && across * down > kCus ? kCus : across * down;
+    hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, LONG, TO>), dim3((unsigned)groups),
                        dim3(64 * WM * WN), 0, (hipStream_t)stream, job);
     return (int)hipGetLastError();
 }
@@ -618,12 +736,13 @@ int product(const GroupedJob& job, void* stream) {
     const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
     const bool ok = direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) &&
                     direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes);
-    if (!ok) return any<T, AT, BT, K, TO>(job, stream);
+    // tiles count rows and columns in 32 bits
+    if (!ok || job.inner > 0x7FFFFF00 || job.outer > 0x7FFFFF00) return any<T, AT, BT, K, TO>(job, stream);
     const int variant = pick_tile<K>(job);
     switch (variant) {
-        case 0: return tile<T, AT, BT, K, 256, 256, 2, 4, 4, TO>(job, stream);
-        case 1: return tile<T, AT, BT, K, 128, 64, 2, 2, 4, TO>(job, stream);
-        default: return tile<T, AT, BT, K, 64, 64, 2, 2, 4, TO>(job, stream);
+        case 0: return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, TO>(job, stream);
+        case 1: return tile<T, AT, BT, K, 128, 64, 2, 2, 4, false, TO>(job, stream);
+        default: return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, TO>(job, stream);
     }
 }
 

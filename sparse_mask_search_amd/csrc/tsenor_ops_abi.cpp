@@ -22,6 +22,8 @@ bool float_type(int t) { return t == TSENOR_F32 || t == TSENOR_BF16; }
 int64_t element_size(int t) { return t == TSENOR_F32 ? 4 : 2; }
 // rows of four neighbouring entries may be written at once
 bool four(const void* p, int type, int64_t ld) { return !misaligned(p, 4 * element_size(type)) && ld % 4 == 0; }
+// rows of eight bf16 entries
+bool eight(const void* p, int64_t ld) { return !misaligned(p, 16) && ld % 8 == 0; }
 
 int status(int e, const char* where) {
     if (e == kGridTooLarge) return TSENOR_ERR_SHAPE;
@@ -142,6 +144,7 @@ int tsenor_grouped_mm(const uint16_t* X, int64_t rows, int64_t ldx, const uint16
     j.out = Y;
     j.ldo = ldy;
     j.ovec = four(Y, ytype, ldy);
+    j.ovec8 = eight(Y, ldy);
     return status(launch_grouped_mm(j, transpose == 1, ytype == TSENOR_BF16, stream), "grouped_mm kernel launch");
 }
 
@@ -172,7 +175,8 @@ int tsenor_grouped_wgrad(const uint16_t* dY, int64_t lddy, const uint16_t* X, in
     j.out = C;
     j.ldo = ldc;
     j.ostride = stride;
-    j.ovec = four(C, ctype, ldc) && stride % 4 == 0;
+    j.ovec = four(C, ctype, ldc) && (experts == 1 || stride % 4 == 0);
+    j.ovec8 = eight(C, ldc) && (experts == 1 || stride % 8 == 0);
     return status(launch_grouped_wgrad(j, ctype == TSENOR_BF16, stream), "grouped_wgrad kernel launch");
 }
 
@@ -227,6 +231,7 @@ int tsenor_gemm_int8(const void* X, int xtype, const float* xscales, int64_t row
     j.bcols = k;
     j.bvec = !misaligned(X, 16) && ldx % 8 == 0;
     j.ovec = four(Y, ytype, ldy);
+    j.ovec8 = eight(Y, ldy);
     return status(launch_gemm_int8(j, !ready, ytype == TSENOR_BF16, stream), "gemm_int8 kernel launch");
 }
 

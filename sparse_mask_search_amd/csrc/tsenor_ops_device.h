@@ -76,6 +76,8 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
     return __builtin_bit_cast(const uint8_t*, u32x2{(uint32_t)uniform((int)v.x), (uint32_t)uniform((int)v.y)});
 }
 
+constexpr int kMaxExperts = 1024;
+
 // Where the rows of one tile lie.
 struct RowTile {
     int expert;      // -1: rows of no expert
@@ -127,6 +129,54 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
     if (t < 0) return false;
     *to = {-1, last + (t - before) * size, rows};
     return to->first < rows;
+}
+
+// The same from a table in LDS, which the workgroup fills once: for each expert its first tile and
+// its first row, then those of the rows that belong to none.  Returns the number of tiles.
+__device__ __forceinline__ int row_table(const int* ends, int experts, int rows, int size, int* table) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, last = 0;
+    if (ends == nullptr) {
+        before = (rows + size - 1) / size;
+        last = rows;
+        if (threadIdx.x == 0) table[0] = table[1] = 0;
+    } else {
+        for (int e0 = 0; e0 < experts; e0 += 64) {
+            const int e = e0 + lane;
+            const int hi = e < experts ? end_of(ends, e, rows) : 0;
+            int lo = __shfl_up(hi, 1, 64);
+            if (lane == 0) lo = last;
+            const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(sum, d, 64);
+                if (lane >= d) sum += o;
+            }
+            if (e < experts && threadIdx.x < 64) {
+                table[2 * e] = before + sum - n;
+                table[2 * e + 1] = lo;
+            }
+            before += __builtin_amdgcn_readlane(sum, 63);
+            last = __builtin_amdgcn_readlane(hi, min(63, experts - 1 - e0));
+        }
+    }
+    if (threadIdx.x == 0) {
+        table[2 * experts] = before;
+        table[2 * experts + 1] = last;
+    }
+    return before + (rows - last + size - 1) / size;
+}
+__device__ __forceinline__ RowTile row_tile_of(const int* table, int experts, int rows, int size, int t) {
+    const int lane = threadIdx.x & 63;
+    int e = -1;  // the last expert whose first tile is not behind t: those before it with the same one have no rows
+    for (int e0 = 0; e0 <= experts; e0 += 64) {
+        const uint64_t begun = __ballot(e0 + lane <= experts && table[2 * min(e0 + lane, experts)] <= t);
+        e += __builtin_popcountll(begun);
+        if (begun != ~uint64_t(0)) break;
+    }
+    const int first = table[2 * e + 1];
+    return {e == experts ? -1 : e, first + (t - table[2 * e]) * size, e == experts ? rows : table[2 * e + 3]};
 }
 
 // The most tiles that row_tile can give.

@@ -24,7 +24,7 @@ struct GroupedJob {
     int64_t ldo, ostride;  // elements
     int64_t bcols;      // entries of a token's row that is quantised on the way
     bool bvec;          // it may be read 16 bytes at a time
-    bool ovec;          // four neighbouring outputs may be written at once
+    bool ovec, ovec8;   // four (eight bf16) neighbouring outputs may be written at once
 };
 
 // e: types of the operands; transposed: weights [k][m].  They return a hipError_t
