@@ -375,22 +375,32 @@ struct Loads {
     }
 };
 
+// Weight gradients, the largest part of what such a call moves, leave past the caches: 8192 rows of 16
+// experts 2048 x 4096 168 -> 161 us.  A product's results do not (8192 x 4096 over 1024: 60 -> 64 us).
+template <Kind K, class V>
+__device__ __forceinline__ void put_last(V* to, V v) {
+    if constexpr (K == kGradient) __builtin_nontemporal_store(v, to);
+    else *to = v;
+}
+
 // The results of a wave's FA x FB tiles of 16 x 16, rows row0 + STEP j, columns c0 + 16 i + 4 q (c0 a
-// multiple of 32).  Whole tiles: what scales or masks them is loaded first (a load among the
+// multiple of 32).  Where all rows and columns exist, what scales or masks them is loaded first (a load among the
 // stores would wait for all of those before it), and bf16 results of two neighbouring tiles change
 // places between the lane quarters, so that a store has 16 bytes.
 template <class T, Kind K, int FA, int FB, int STEP, class TO>
-__device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, int row0, int rows, int c0, int q,
-                                           const typename T::Sum* sums, TO* out) {
+__device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, int row0, bool complete, int rows, int c0,
+                                           int q, const typename T::Sum* sums, TO* out) {
     constexpr bool kScaled = T::kSize == 1, kMasked = K == kGradient, kHalf = sizeof(TO) == 2;
-    if (c0 + 16 * FA > (int)job.inner || !(kHalf ? job.ovec8 : job.ovec)) {
+    if (!complete || c0 + 16 * FA > (int)job.inner || !(kHalf ? job.ovec8 : job.ovec)) {
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
             const int row = row0 + STEP * j;
             if (row >= rows) continue;
 #pragma unroll
-            for (int i = 0; i < FA; ++i)
+            for (int i = 0; i < FA; ++i) {
+                __builtin_amdgcn_sched_barrier(0);  // or results of several stores are made at once, and spilled
                 finish<T, K>(job, expert, row, c0 + 16 * i + 4 * q, sums[i * FB + j], out + row * job.ldo);
+            }
         }
         return;
     }
@@ -404,13 +414,13 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
 #pragma unroll
             for (int e = 0; e < 4; ++e) across[i][e] = as[16 * i + e];
 #pragma unroll
-        for (int j = 0; j < FB; ++j) down[j] = job.bs[min(row0 + STEP * j, rows - 1)];
+        for (int j = 0; j < FB; ++j) down[j] = job.bs[row0 + STEP * j];
     }
     if constexpr (kMasked) {
         const int64_t words = (job.inner + 31) / 32;
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
-            const uint32_t* row = job.mask + (expert * job.outer + min(row0 + STEP * j, rows - 1)) * words + (c0 >> 5);
+            const uint32_t* row = job.mask + (expert * job.outer + row0 + STEP * j) * words + (c0 >> 5);
 #pragma unroll
             for (int i = 0; i < FA / 2; ++i) keep[j][i] = job.mask == nullptr ? 0xFFFFFFFFu : row[i];
         }
@@ -420,7 +430,7 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
     for (int j = 0; j < FB; ++j) {
 #pragma unroll
         for (int i = 0; i < FA; i += 2) {
-            __builtin_amdgcn_sched_barrier(0);  // or results of several stores are made at once, and spilled
+            __builtin_amdgcn_sched_barrier(0);
             f32x4 v[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p)
@@ -436,10 +446,10 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
                                                                   pack_bf16(v[1][0], v[1][1]), false, false);
                 const u32x2 hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][2], v[0][3]),
                                                                   pack_bf16(v[1][2], v[1][3]), false, false);
-                if (row0 + STEP * j < rows) *reinterpret_cast<u32x4*>(y + 16 * i) = u32x4{lo.x, hi.x, lo.y, hi.y};
-            } else if (row0 + STEP * j < rows) {
+                put_last<K>(reinterpret_cast<u32x4*>(y + 16 * i), u32x4{lo.x, hi.x, lo.y, hi.y});
+            } else {
 #pragma unroll
-                for (int p = 0; p < 2; ++p) *reinterpret_cast<f32x4*>(y + 16 * (i + p)) = v[p];
+                for (int p = 0; p < 2; ++p) put_last<K>(reinterpret_cast<f32x4*>(y + 16 * (i + p)), v[p]);
             }
         }
         y += STEP * job.ldo;
@@ -448,16 +458,16 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
 
 // Work t of `count` for workgroup `bid`: workgroups go to the chip's 8 XCDs round robin and each
 // XCD has its own L2, so XCD x gets a contiguous range.
-__device__ __forceinline__ int64_t in_order(int64_t bid, int64_t count) {
-    const int64_t x = bid % 8, rest = count % 8;
-    return x * (count / 8) + (x < rest ? x : rest) + bid / 8;
+__device__ __forceinline__ int in_order(int bid, int count) {
+    const int x = bid % 8, rest = count % 8;
+    return x * (count / 8) + min(x, rest) + bid / 8;
 }
 // Tile t of a grid, in groups of up to 8 tm column by column: a range forms a compact block.
-__device__ __forceinline__ void grid_tile(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
-    const int64_t grp = t / (8 * tiles_n), first = grp * 8, gm = min(tiles_m - first, (int64_t)8);
-    const int64_t r = t - grp * 8 * tiles_n;
-    tm = first + r % gm;
-    tn = r / gm;
+__device__ __forceinline__ void grid_tile(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int grp = t / (8 * tiles_n), first = grp * 8, gm = min(tiles_m - first, 8);
+    const int r = t - grp * 8 * tiles_n;
+    tm = uniform(first + r % gm);
+    tn = uniform(r / gm);
 }
 
 // Whether a step's loads may meet the reduction's end.
@@ -477,13 +487,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
     constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
     typedef Loads<T, AT, TM, W> LoadsA;
     typedef Loads<T, BT, TN, W> LoadsB;
-    static_assert(R == 4, "a tile has at least R steps");
+    static_assert(R >= 4, "ring");
     struct Buffer {
         u32x4 a[TM * 4];
         u32x4 b[TN * 4];
     };
     __shared__ Buffer ring[R];
-    __shared__ int table[LONG ? 2 * (kMaxExperts + 1) : 1];  // first tile and first row of each expert
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -496,47 +505,61 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         LoadsA la;
         LoadsB lb;
     };
-    int64_t total, work = blockIdx.x;  // tiles of the launch; this workgroup's next one
-    if constexpr (K == kProduct) {
-        int tiles;
+    int total, work = blockIdx.x;  // work of the launch (it fits a grid); this workgroup's next piece
+    int tiles = 0;                                // row tiles
+    if constexpr (K == kProduct && LONG) {
+        tiles = row_table(job.ends, job.experts, job.rows, TN, lds<RowTable>());
+        __syncthreads();
+        total = across * uniform(tiles);
+    } else if constexpr (K == kProduct) {
         RowTile none;
-        if constexpr (LONG) {
-            tiles = row_table(job.ends, job.experts, job.rows, TN, table);
-            __syncthreads();
-        } else {
-            row_tile(job.ends, job.experts, job.rows, TN, -1, &none, &tiles);
-        }
-        total = (int64_t)across * uniform(tiles);
+        row_tile(job.ends, job.experts, job.rows, TN, -1, &none, &tiles);
+        total = across * uniform(tiles);
     } else {
-        total = (int64_t)across * down * job.experts;
+        total = across * down * job.experts;
+        if constexpr (LONG) {
+            expert_rows(job.ends, job.experts, job.rows, lds<ExpertRows>());
+            __syncthreads();
+        }
     }
     // The next tile that has something to add up; the others' results are zeros, written here.
     const auto find = [&](Tile& to) __attribute__((always_inline)) {
-        for (; work < total; work += LONG ? (int64_t)gridDim.x : total) {
+        for (; work < total; work += LONG ? (int)gridDim.x : total) {
             const uint8_t *a = static_cast<const uint8_t*>(job.a), *b = static_cast<const uint8_t*>(job.b);
-            int64_t tm, tn;
+            int tm = 0, tn = 0;
             if constexpr (K == kProduct) {
                 RowTile t;
-                grid_tile(in_order(work, total), across, total / across, tm, tn);
-                if constexpr (LONG) t = row_tile_of(table, job.experts, job.rows, TN, uniform((int)tn));
-                else row_tile(job.ends, job.experts, job.rows, TN, uniform((int)tn), &t);
+                grid_tile(in_order(work, total), across, uniform(tiles), tm, tn);
+                if constexpr (LONG) t = row_tile_of(lds<RowTable>(), job.experts, job.rows, TN, tn);
+                else row_tile(job.ends, job.experts, job.rows, TN, tn, &t);
                 to.expert = uniform(t.expert);
-                to.inner0 = uniform((int)tm) * TM;
+                to.inner0 = tm * TM;
                 to.outer0 = uniform(t.first);
                 to.outer_end = uniform(t.end);
                 to.reduce = to.expert < 0 ? 0 : job.kbytes;
                 a += to.expert * job.astride + (AT ? (int64_t)to.inner0 * T::kSize : to.inner0 * job.lda);
                 b += to.outer0 * job.ldb;
             } else {
-                // expert after expert, each spread over all XCDs: they may have very different numbers of rows
-                const int64_t per = (int64_t)across * down;
-                to.expert = uniform((int)(work / per));
-                grid_tile(in_order(work % per, per), across, down, tm, tn);
-                to.inner0 = uniform((int)tm) * TM;
-                to.outer0 = uniform((int)tn) * TN;
+                // Expert after expert, each spread over all XCDs.  Workgroups that take many tiles go
+                // through the experts by falling numbers of rows, every other round the other way, so
+                // that all add up about as many rows.
+                const int per = across * down, g = gridDim.x, round = work / g;
+                int w = work;
+                if (LONG && round % 2 == 1 && (round + 1) * g <= total) w = (2 * round + 1) * g - 1 - work;
+                to.expert = uniform(w / per);
+                if constexpr (LONG) {
+                    if (job.experts <= 64) to.expert = uniform(lds<ExpertRows>().order[to.expert]);
+                }
+                grid_tile(in_order(w % per, per), across, down, tm, tn);
+                to.inner0 = tm * TM;
+                to.outer0 = tn * TN;
                 to.outer_end = (int)job.outer;
-                const int first = uniform(to.expert == 0 ? 0 : end_of(job.ends, to.expert - 1, job.rows));
-                to.reduce = (int64_t)uniform(max(end_of(job.ends, to.expert, job.rows) - first, 0)) * T::kSize;
+                const auto end = [&](int e) __attribute__((always_inline)) {
+                    if constexpr (LONG) return lds<ExpertRows>().end[e];
+                    else return end_of(job.ends, e, job.rows);
+                };
+                const int first = uniform(to.expert == 0 ? 0 : end(to.expert - 1));
+                to.reduce = (int64_t)uniform(max(end(to.expert) - first, 0)) * T::kSize;
                 a += first * job.lda + (int64_t)to.inner0 * T::kSize;
                 b += first * job.ldb + (int64_t)to.outer0 * T::kSize;
             }
@@ -548,10 +571,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
                 continue;
             }
             to.full = (int)(to.reduce / 64);
-            to.steps = max(2 * (int)((to.reduce + 127) / 128), R);
+            to.steps = max(2 * (int)((to.reduce + 127) / 128), (R + 1) / 2 * 2);  // R at least: loads reach into one tile behind
             to.la.init(a, job.lda, (int)min(job.inner - to.inner0, (int64_t)TM), wave, lane);
             to.lb.init(b, job.ldb, min(to.outer_end - to.outer0, TN), wave, lane);
-            work += LONG ? (int64_t)gridDim.x : total;
+            work += LONG ? (int)gridDim.x : total;
             return true;
         }
         return false;
@@ -665,8 +688,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         if (K == kProduct && TB > 1 && cur.outer_end - cur.outer0 <= TN / 2) all_steps(Count<TB / 2 + (TB == 1)>());
         else all_steps(Count<TB>());
         const int row0 = cur.outer0 + 16 * wn + (lane & 15), c0 = cur.inner0 + (TM / WM) * wm;
-        store_tile<T, K, 2 * TA, 2 * TB, 16 * WN>(job, cur.expert, row0, cur.outer_end, c0, lane >> 4, &acc[0][0][0][0],
-                                         static_cast<TO*>(job.out) + (K == kGradient ? cur.expert * job.ostride : 0));
+        store_tile<T, K, 2 * TA, 2 * TB, 16 * WN>(
+            job, cur.expert, row0, cur.outer_end - cur.outer0 >= TN, cur.outer_end, c0, lane >> 4, &acc[0][0][0][0],
+            static_cast<TO*>(job.out) + (K == kGradient ? cur.expert * job.ostride : 0));
         if (!more) break;
         cur = nxt;
         more = find(nxt);
@@ -710,17 +734,20 @@ int tile(const GroupedJob& job, void* stream) {
     const int64_t down = K == kGradient ? (job.outer + TN - 1) / TN * job.experts
                                         : most_row_tiles(job.rows, job.experts, TN, job.ends != nullptr);
     if (across > (int64_t)0xFFFFFFFF / (64 * WM * WN) / down) return kGridTooLarge;
-    const int64_t groups = LONG && across * down > kCus ? kCus : across * down;
+    const int64_t most = kCus * (sizeof(u32x4) * 4 * (TM + TN) * R > 72 * 1024 ? 1 : 2);
+    const int64_t groups = LONG && across * down > most ? most : across * down;
     hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, LONG, TO>), dim3((unsigned)groups),
                        dim3(64 * WM * WN), 0, (hipStream_t)stream, job);
     return (int)hipGetLastError();
 }
 
-// The largest tile that leaves every CU a workgroup, counting half a tile more for each expert:
-// 0: 256 x 256, 1: 128 x 64, 2: 64 x 64.  Measured (us) for 0 / 1 / 2: 16384 rows of 8 experts 11008 x
-// 4096: 1395 / 2568 / 3217; 1003 rows of 16 experts 2048 x 4096: 100 / 88 / 89; 200 rows of them: 86 / 65 /
-// 65; weight gradients, 8192 rows of 16 experts 2048 x 4096: 237 / 306 / 351; 1001 rows of 4 1024 x 1024: 22 /
-// 11 / 11.
+// Tiles: 0: 256 x 256; 1: 256 x 128, a ring of six; 2: 64 x 64, a ring of eight; 3: 64 x 64, four.  The
+// larger ones need about 160 workgroups (half a tile more counted for each expert); 2 is for experts with
+// few rows, where reading the weights bounds.  Measured (us) for 0 / 1 / 2 / 3: 16384 rows of 8 experts
+// 11008 x 4096: 1252 / 1645 / 3972 / 3152; 4096 rows of 16 experts 2048 x 4096 (192 tiles of 256 x 256): 116 / 153 /
+// 203 / 198; 2048 rows (192 of 256 x 128): 111 / 94 / 130 / 133; 1003 rows: 101 / 93 / 83 / 90; 100 rows: 82 /
+// 77 / 60 / 64; 512 rows 4096 x 4096: 74 / 53 / 38 / 35; weight gradients, 2048 rows of 8 experts 1024 x 2048 (256
+// tiles): 23 / 25 / 43 / 29; 1001 rows of 4 experts 1024 x 1024: 21 / 15 / 13 / 11.
 template <Kind K>
 int pick_tile(const GroupedJob& job) {
     const auto tiles = [&](int64_t m, int64_t n) {
@@ -728,7 +755,9 @@ int pick_tile(const GroupedJob& job) {
         return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
                                         : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts / 2 : 0));
     };
-    return tiles(256, 256) >= 256 ? 0 : tiles(128, 64) >= 256 ? 1 : 2;
+    if (tiles(256, 256) >= 160) return 0;
+    if (K == kProduct && tiles(256, 128) >= 160) return 1;
+    return K == kProduct && job.rows <= 64 * (int64_t)job.experts ? 2 : 3;
 }
 
 template <class T, bool AT, bool BT, Kind K, class TO>
@@ -739,11 +768,12 @@ int product(const GroupedJob& job, void* stream) {
     // tiles count rows and columns in 32 bits
     if (!ok || job.inner > 0x7FFFFF00 || job.outer > 0x7FFFFF00) return any<T, AT, BT, K, TO>(job, stream);
     const int variant = pick_tile<K>(job);
-    switch (variant) {
-        case 0: return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, TO>(job, stream);
-        case 1: return tile<T, AT, BT, K, 128, 64, 2, 2, 4, false, TO>(job, stream);
-        default: return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, TO>(job, stream);
+    if (variant == 0) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, TO>(job, stream);
+    if constexpr (K == kProduct) {
+        if (variant == 1) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, TO>(job, stream);
+        if (variant == 2) return tile<T, AT, BT, K, 64, 64, 2, 2, 8, true, TO>(job, stream);
     }
+    return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, TO>(job, stream);
 }
 
 }  // namespace

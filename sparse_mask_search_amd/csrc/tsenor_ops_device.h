@@ -131,52 +131,73 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
     return to->first < rows;
 }
 
+// One T of the workgroup in LDS.
+template <class T>
+__device__ __forceinline__ T& lds() {
+    __shared__ T one;
+    return one;
+}
+
+// The rows of all experts, and up to 64 experts by falling numbers of rows (ties in order).
+struct ExpertRows {
+    int end[kMaxExperts], order[64];
+};
+__device__ __forceinline__ void expert_rows(const int* ends, int experts, int rows, ExpertRows& table) {
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) table.end[e] = end_of(ends, e, rows);
+    if (experts > 64) return;
+    const int lane = threadIdx.x & 63;
+    const int hi = lane < experts ? end_of(ends, lane, rows) : 0, lo = __shfl_up(hi, 1, 64);
+    const int n = lane < experts ? hi - (lane == 0 ? 0 : lo) : 0;
+    int rank = 0;
+    for (int e = 0; e < experts; ++e) {
+        const int o = __builtin_amdgcn_readlane(n, e);
+        rank += o > n || (o == n && e < lane) ? 1 : 0;
+    }
+    if (threadIdx.x < experts) table.order[rank] = lane;
+}
+
 // The same from a table in LDS, which the workgroup fills once: for each expert its first tile and
 // its first row, then those of the rows that belong to none.  Returns the number of tiles.
-__device__ __forceinline__ int row_table(const int* ends, int experts, int rows, int size, int* table) {
+struct RowTable {
+    int tile[kMaxExperts + 1], row[kMaxExperts + 1];
+};
+__device__ __forceinline__ int row_table(const int* ends, int experts, int rows, int size, RowTable& table) {
     const int lane = threadIdx.x & 63;
     int before = 0, last = 0;
-    if (ends == nullptr) {
-        before = (rows + size - 1) / size;
-        last = rows;
-        if (threadIdx.x == 0) table[0] = table[1] = 0;
-    } else {
-        for (int e0 = 0; e0 < experts; e0 += 64) {
-            const int e = e0 + lane;
-            const int hi = e < experts ? end_of(ends, e, rows) : 0;
-            int lo = __shfl_up(hi, 1, 64);
-            if (lane == 0) lo = last;
-            const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
-            int sum = n;
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        const int e = e0 + lane;
+        const int hi = e >= experts ? 0 : ends == nullptr ? rows : end_of(ends, e, rows);
+        int lo = __shfl_up(hi, 1, 64);
+        if (lane == 0) lo = last;
+        const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
+        int sum = n;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(sum, d, 64);
-                if (lane >= d) sum += o;
-            }
-            if (e < experts && threadIdx.x < 64) {
-                table[2 * e] = before + sum - n;
-                table[2 * e + 1] = lo;
-            }
-            before += __builtin_amdgcn_readlane(sum, 63);
-            last = __builtin_amdgcn_readlane(hi, min(63, experts - 1 - e0));
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += o;
         }
+        if (e < experts && threadIdx.x < 64) {
+            table.tile[e] = before + sum - n;
+            table.row[e] = lo;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+        last = __builtin_amdgcn_readlane(hi, min(63, experts - 1 - e0));
     }
     if (threadIdx.x == 0) {
-        table[2 * experts] = before;
-        table[2 * experts + 1] = last;
+        table.tile[experts] = before;
+        table.row[experts] = last;
     }
     return before + (rows - last + size - 1) / size;
 }
-__device__ __forceinline__ RowTile row_tile_of(const int* table, int experts, int rows, int size, int t) {
+__device__ __forceinline__ RowTile row_tile_of(const RowTable& table, int experts, int rows, int size, int t) {
     const int lane = threadIdx.x & 63;
     int e = -1;  // the last expert whose first tile is not behind t: those before it with the same one have no rows
     for (int e0 = 0; e0 <= experts; e0 += 64) {
-        const uint64_t begun = __ballot(e0 + lane <= experts && table[2 * min(e0 + lane, experts)] <= t);
+        const uint64_t begun = __ballot(e0 + lane <= experts && table.tile[min(e0 + lane, experts)] <= t);
         e += __builtin_popcountll(begun);
         if (begun != ~uint64_t(0)) break;
     }
-    const int first = table[2 * e + 1];
-    return {e == experts ? -1 : e, first + (t - table[2 * e]) * size, e == experts ? rows : table[2 * e + 3]};
+    return {e == experts ? -1 : e, table.row[e] + (t - table.tile[e]) * size, e == experts ? rows : table.row[e + 1]};
 }
 
 // The most tiles that row_tile can give.
