@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "tsenor_internal.h"
 #include "tsenor_ops_device.h"
 
@@ -369,6 +371,21 @@ struct Loads {
         const uint8_t* p = at < reduce ? of.base + s * of.step + of.offset[j] : reinterpret_cast<const uint8_t*>(&kZeros);
         dma16_at(p, to);
     }
+    // The same through a register, at any alignment (not turned); store() puts it where load() would.
+    __device__ static __forceinline__ u32x4 fetch(const Loads& of, bool inside, int j, int64_t s, int64_t reduce, int wave,
+                                                  int lane) {
+        const uint8_t* p = of.base + s * of.step + of.offset[j];
+        if (inside) {
+            u32x4 v;
+            __builtin_memcpy(&v, p, 16);
+            return v;
+        }
+        const int slot = 64 * (wave * kCount + j) + lane, r = slot / 4;
+        return load16<T>(p, reduce - 64 * s - 16 * (row_slot(r, slot % 4) - 4 * r));
+    }
+    __device__ static __forceinline__ void store(u32x4* tile, int j, u32x4 v, int wave, int lane) {
+        tile[64 * (wave * kCount + j) + lane] = v;
+    }
     __device__ static __forceinline__ u32x4 fragment(const u32x4* tile, int at, int lane) {
         if constexpr (TURNED) return turned_fragment<S>(tile, at, lane);
         else return row_fragment(tile, at, lane);
@@ -482,12 +499,12 @@ struct Count {
     static constexpr int value = N;
 };
 
-template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, class TO>
+template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, bool DIRECT, class TO>
 __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const GroupedJob job) {
     constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
     typedef Loads<T, AT, TM, W> LoadsA;
     typedef Loads<T, BT, TN, W> LoadsB;
-    static_assert(R >= 4, "ring");
+    static_assert(DIRECT ? R >= 4 : R == 3 && !AT && !BT, "ring");
     struct Buffer {
         u32x4 a[TM * 4];
         u32x4 b[TN * 4];
@@ -571,7 +588,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
                 continue;
             }
             to.full = (int)(to.reduce / 64);
-            to.steps = max(2 * (int)((to.reduce + 127) / 128), (R + 1) / 2 * 2);  // R at least: loads reach into one tile behind
+            to.steps = max(2 * (int)((to.reduce + 127) / 128), R < 4 ? 4 : (R + 1) / 2 * 2);  // loads reach into one tile behind
             to.la.init(a, job.lda, (int)min(job.inner - to.inner0, (int64_t)TM), wave, lane);
             to.lb.init(b, job.ldb, min(to.outer_end - to.outer0, TN), wave, lane);
             work += LONG ? (int)gridDim.x : total;
@@ -598,6 +615,23 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             LoadsB::load(ahead ? nxt.lb : cur.lb, inside, j - LoadsA::kCount, s, ahead ? nxt.reduce : cur.reduce, buf.b,
                          wave, lane);
     };
+    // Not DIRECT: what step t + 1 needs is written to LDS in the first half of step t, and what step t + 3
+    // needs is fetched into the same registers in the second.
+    u32x4 held[DIRECT ? 1 : 2][DIRECT ? 1 : kLoads];
+    const auto fetch = [&](auto end, int j, int t, int set) __attribute__((always_inline)) {
+        const bool ahead = end.value && t >= cur.steps;
+        const int s = ahead ? t - cur.steps : t;
+        const bool inside = !end.value || s < (ahead ? nxt.full : cur.full);
+        if (j < LoadsA::kCount)
+            held[set][j] = LoadsA::fetch(ahead ? nxt.la : cur.la, inside, j, s, ahead ? nxt.reduce : cur.reduce, wave, lane);
+        else
+            held[set][j] = LoadsB::fetch(ahead ? nxt.lb : cur.lb, inside, j - LoadsA::kCount, s,
+                                         ahead ? nxt.reduce : cur.reduce, wave, lane);
+    };
+    const auto store = [&](int j, int set, Buffer& buf) __attribute__((always_inline)) {
+        if (j < LoadsA::kCount) LoadsA::store(buf.a, j, held[set][j], wave, lane);
+        else LoadsB::store(buf.b, j - LoadsA::kCount, held[set][j], wave, lane);
+    };
     typename T::Sum acc[TA][2][TB][2];  // pairs of 16: tiles of 32 x 32
     u32x4 fa[2][2], fb[2][TB][2];
     const auto read_a = [&](int i, const Buffer& buf) __attribute__((always_inline)) {  // into the set i & 1
@@ -614,13 +648,14 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
     };
     // Step t, whose first operands are in registers (set t & 1).  The loads of step t + R - 1 go
     // out after the barrier, the last kLate of them in the first half of the next step.
-    const auto step = [&](auto end, auto pairs, int t, int set, const Buffer& buf, const Buffer& next, Buffer& early,
+    const auto step = [&](auto end, auto pairs, int t, int set, const Buffer& buf, Buffer& next, Buffer& early,
                           Buffer& late) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < TA; ++i) {
             if (i == TA / 2) {
                 // the next step's loads have landed, and every wave is past the step before
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 3) * kLoads) : "memory");
+                if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 3) * kLoads) : "memory");
+                else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
@@ -641,7 +676,15 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
                 __builtin_amdgcn_sched_barrier(0);
                 constexpr int kSlots = TA > 1 ? TA / 2 * pairs.value : pairs.value;  // of a half step
                 const int slot = (i >= TA / 2 ? i - TA / 2 : i) * pairs.value + j;
-                if (i >= TA / 2) {
+                if constexpr (!DIRECT) {
+                    if (i >= TA / 2) {
+#pragma unroll
+                        for (int l = slot; l < kLoads; l += kSlots) fetch(end, l, t + 3, set ^ 1);
+                    } else {
+#pragma unroll
+                        for (int l = slot; l < kLoads; l += kSlots) store(l, set ^ 1, next);
+                    }
+                } else if (i >= TA / 2) {
 #pragma unroll
                     for (int l = slot; l < kLoads - kLate; l += kSlots) load(end, l, t + R - 1, early);
                 } else {
@@ -654,13 +697,28 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-#pragma unroll
-    for (int t = 0; t < R - 1; ++t)
-#pragma unroll
-        for (int j = 0; j < (t == R - 2 ? kLoads - kLate : kLoads); ++j) load(AtEnd(), j, t, ring[t]);
     bool more = false;
-    if constexpr (LONG) more = find(nxt);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 2) * kLoads - kLate) : "memory");
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int t = 0; t < R - 1; ++t)
+#pragma unroll
+            for (int j = 0; j < (t == R - 2 ? kLoads - kLate : kLoads); ++j) load(AtEnd(), j, t, ring[t]);
+        if constexpr (LONG) more = find(nxt);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((R - 2) * kLoads - kLate) : "memory");
+    } else {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            fetch(AtEnd(), j, 0, 0);
+            fetch(AtEnd(), j, 1, 1);
+        }
+        if constexpr (LONG) more = find(nxt);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            store(j, 0, ring[0]);
+            fetch(AtEnd(), j, 2, 0);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     read_b(Count<TB>(), 0, ring[0]);
@@ -681,7 +739,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             at = two;
         };
         const auto all_steps = [&](auto pairs) __attribute__((always_inline)) {
-            for (; t + R < cur.full; t += 2) two_steps(Inside(), pairs);
+            // two steps reach as far as t + R (DIRECT) or t + 4
+            for (; t + (DIRECT ? R : 4) < cur.full; t += 2) two_steps(Inside(), pairs);
             for (; t < cur.steps; t += 2) two_steps(AtEnd(), pairs);
         };
         // an expert's last rows fill half a tile at most as often as not
@@ -725,18 +784,25 @@ int few(const GroupedJob& job, void* stream) {
 
 // Direct loads take 16 bytes of an aligned row at a time.
 bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0 && ld < kMaxRow;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0;
 }
 
-template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, class TO>
+template <Kind K>
+int64_t tiles_of(const GroupedJob& job, int64_t m, int64_t n) {  // half a tile more counted for each expert
+    const int64_t across = (job.inner + m - 1) / m;
+    return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
+                                    : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts / 2 : 0));
+}
+
+template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, bool DIRECT, class TO>
 int tile(const GroupedJob& job, void* stream) {
     const int64_t across = (job.inner + TM - 1) / TM;
     const int64_t down = K == kGradient ? (job.outer + TN - 1) / TN * job.experts
                                         : most_row_tiles(job.rows, job.experts, TN, job.ends != nullptr);
     if (across > (int64_t)0xFFFFFFFF / (64 * WM * WN) / down) return kGridTooLarge;
-    const int64_t most = kCus * (sizeof(u32x4) * 4 * (TM + TN) * R > 72 * 1024 ? 1 : 2);
+    const int64_t most = kCus * (sizeof(u32x4) * 4 * (TM + TN) * R > 72 * 1024 ? 1 : 2);  // by LDS
     const int64_t groups = LONG && across * down > most ? most : across * down;
-    hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, LONG, TO>), dim3((unsigned)groups),
+    hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, LONG, DIRECT, TO>), dim3((unsigned)groups),
                        dim3(64 * WM * WN), 0, (hipStream_t)stream, job);
     return (int)hipGetLastError();
 }
@@ -750,30 +816,45 @@ int tile(const GroupedJob& job, void* stream) {
 // tiles): 23 / 25 / 43 / 29; 1001 rows of 4 experts 1024 x 1024: 21 / 15 / 13 / 11.
 template <Kind K>
 int pick_tile(const GroupedJob& job) {
-    const auto tiles = [&](int64_t m, int64_t n) {
-        const int64_t across = (job.inner + m - 1) / m;
-        return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
-                                        : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts / 2 : 0));
-    };
-    if (tiles(256, 256) >= 160) return 0;
-    if (K == kProduct && tiles(256, 128) >= 160) return 1;
+    if (tiles_of<K>(job, 256, 256) >= 160) return 0;
+    if (K == kProduct && tiles_of<K>(job, 256, 128) >= 160) return 1;
     return K == kProduct && job.rows <= 64 * (int64_t)job.experts ? 2 : 3;
 }
 
 template <class T, bool AT, bool BT, Kind K, class TO>
 int product(const GroupedJob& job, void* stream) {
-    const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
-    const bool ok = direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) &&
-                    direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes);
-    // tiles count rows and columns in 32 bits
-    if (!ok || job.inner > 0x7FFFFF00 || job.outer > 0x7FFFFF00) return any<T, AT, BT, K, TO>(job, stream);
-    const int variant = pick_tile<K>(job);
-    if (variant == 0) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, TO>(job, stream);
-    if constexpr (K == kProduct) {
-        if (variant == 1) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, TO>(job, stream);
-        if (variant == 2) return tile<T, AT, BT, K, 64, 64, 2, 2, 8, true, TO>(job, stream);
+    if constexpr (K == kProduct && !AT) {
+        // Few rows: on average up to eight an expert, or up to 64 where tiles would leave CUs without work.
+        // Measured (us), 16 columns a wave / 64 x 64 tiles: 6 rows of 64 experts 1408 x 2048: 11 / 28; 64 rows:
+        // 47 / 47; 64 rows of 16 experts 2048 x 4096: 49 / 56; 16 rows 11008 x 4096: 21 / 24; 64 rows 4096 x
+        // 4096 18 / 25, 11008 x 4096 46 / 25.  As many columns as leave 160 workgroups: one row 4096 x 4096 in
+        // 11 / 13 / 19 for 16 / 32 / 64; 16 rows 11008 x 4096 in 26 / 28 / 21.
+        const int64_t parts = job.ends != nullptr ? std::min<int64_t>(job.rows, job.experts) : 1;
+        if (job.rows <= 16 || job.rows <= 8 * (int64_t)job.experts) {
+            if ((job.inner + 63) / 64 * parts >= 160) return few<T, false, 1, 4, TO>(job, stream);
+            if ((job.inner + 31) / 32 * parts >= 160) return few<T, false, 1, 2, TO>(job, stream);
+            return few<T, false, 1, 1, TO>(job, stream);
+        }
+        if (job.rows <= 64 && tiles_of<K>(job, 64, 64) < 128) return few<T, false, 2, 2, TO>(job, stream);
     }
-    return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, TO>(job, stream);
+    // tiles count rows, columns and the bytes between rows in 32 bits
+    if (job.inner > 0x7FFFFF00 || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow || job.ldb >= kMaxRow)
+        return any<T, AT, BT, K, TO>(job, stream);
+    const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
+    if (!direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) ||
+        !direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes)) {
+        // 16384 rows of 8 experts 11009 x 4095: 5855 us in tiles of 64 x 64, 3613 in tiles of 256 x 128
+        if constexpr (!AT && !BT)
+            if (tiles_of<K>(job, 256, 128) >= 160) return tile<T, AT, BT, K, 256, 128, 2, 4, 3, true, false, TO>(job, stream);
+        return any<T, AT, BT, K, TO>(job, stream);
+    }
+    const int variant = pick_tile<K>(job);
+    if (variant == 0) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, true, TO>(job, stream);
+    if constexpr (K == kProduct) {
+        if (variant == 1) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, true, TO>(job, stream);
+        if (variant == 2) return tile<T, AT, BT, K, 64, 64, 2, 2, 8, true, true, TO>(job, stream);
+    }
+    return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, true, TO>(job, stream);
 }
 
 }  // namespace
