@@ -84,8 +84,8 @@ int tsenor_quant_int8(const void* X, int dtype, int64_t batch, int64_t stride, i
  * [rows][k] and A (a batch of `experts` operands [m][k]), sums exact in 32 bits;
  * Y[r][j] = round(float(sum) * xs[r] * as[j]), left to right in fp32.
  *   X      xtype TSENOR_INT8: values of an operand, and its scales;
- *          xtype TSENOR_BF16: [rows][ldx] with rows <= 16 and ends NULL, quantised
- *          on the way as tsenor_quant_int8 does, xscales NULL;
+ *          xtype TSENOR_BF16: [rows][ldx] with rows <= 16, rows * kpad <= 2^15 and ends
+ *          NULL, quantised on the way as tsenor_quant_int8 does, xscales NULL;
  *   ldx    kpad for TSENOR_INT8, >= k for TSENOR_BF16;
  *   ends   as above, or NULL: one weight (experts 1) for all rows;
  *   Y      ytype f32 or bf16, [rows][ldy], ldy >= m.

@@ -199,7 +199,7 @@ def gemm_int8(torch, X, A, ends=None, out=None, dtype=None):
     yt = _float_type(torch, out, "out")
     if rows == 0 or m == 0:
         return out
-    if not ready and xt == BF16 and rows <= 16 and ends is None:
+    if not ready and xt == BF16 and ends is None and rows <= 16 and rows * _pad(k) <= 32768:
         x, xtype, xs, ldx = X, BF16, None, _ld(X)
     else:
         q = X if ready else _quantised(torch, X)
@@ -222,46 +222,9 @@ def _as_rows(t, name):
 
 def _as_any(t, name):
     """A gradient without a mask: its entries in any order."""
-    if t.is_contiguous():
-        return 1, t.numel(), t.numel()
     if t.dim() == 2 and t.stride(1) != 1 and t.stride(0) == 1 and t.stride(1) >= t.shape[0]:
         return t.shape[1], t.shape[0], t.stride(1)  # column by column
     return _as_rows(t, name)
-
-
-def _grad_list(torch, grads, masks, out):
-    """The C descriptors of a list of gradients (eight 64-bit words each)."""
-    if not isinstance(grads, (list, tuple)):
-        raise TypeError("grads must be a list of tensors")
-    n = len(grads)
-    if masks is not None and len(masks) != n:
-        raise ValueError("masks must hold one entry (a mask or None) per gradient")
-    if out is not None and len(out) != n:
-        raise ValueError("out must hold one tensor per gradient")
-    device, words = grads[0].device, []
-    f32, bf16 = torch.float32, torch.bfloat16
-    for i, g in enumerate(grads):
-        if not isinstance(g, torch.Tensor) or g.device != device:
-            raise TypeError(f"grads[{i}] must be a tensor on {device}")
-        if g.dtype is not f32 and g.dtype is not bf16:
-            raise TypeError(f"grads[{i}] must be float32 or bfloat16")
-        m = None if masks is None else masks[i]
-        if m is not None:
-            if g.dim() == 0:
-                raise ValueError(f"grads[{i}] has a mask and no columns")
-            _part(torch, m, torch.int32, (*g.shape[:-1], (g.shape[-1] + 31) // 32), device, f"masks[{i}]")
-        o = g if out is None else out[i]
-        if o is not g and (not isinstance(o, torch.Tensor) or o.device != device or o.dtype != g.dtype
-                           or o.shape != g.shape):
-            raise ValueError(f"out[{i}] must be a tensor like grads[{i}]")
-        if m is None and (o is g or o.stride() == g.stride()):
-            rows, cols, ld = _as_any(g, f"grads[{i}]")
-            ldo = ld
-        else:
-            rows, cols, ld = _as_rows(g, f"grads[{i}]")
-            ldo = ld if o is g else _as_rows(o, f"out[{i}]")[2]
-        words += (g.data_ptr(), o.data_ptr(), 0 if m is None else m.data_ptr(), F32 if g.dtype is f32 else BF16, rows, cols, ld, ldo)
-    return device, words
 
 
 def _matrix_of(t):
@@ -269,19 +232,17 @@ def _matrix_of(t):
     return t.t() if t.dim() == 2 and t.stride(1) != 1 and t.stride(0) == 1 else t
 
 
-def _no_two(grads, masks, out):
-    """Refuses lists in which something that is written shares bytes with anything else."""
-    spans = []
-    for i, g in enumerate(grads):
-        if g.numel() == 0:
-            continue
-        o = g if out is None else out[i]
-        spans.append((o.data_ptr(), _last(o), True, o))
-        if o is not g and o.data_ptr() != g.data_ptr():
-            spans.append((g.data_ptr(), _last(g), False, g))
-        if masks is not None and masks[i] is not None:
-            spans.append((masks[i].data_ptr(), _last(masks[i]), False, masks[i]))
+def _no_two(spans):
+    """Refuses spans (first byte, byte behind the last, written, tensor) of which one that is written
+    shares bytes with another."""
     spans.sort(key=lambda s: s[:2])
+    end = 0
+    for s in spans:
+        if s[0] < end:
+            break
+        end = s[1]
+    else:
+        return  # all apart
     open_, end = [], 0
     for s in spans:
         if s[0] >= end:
@@ -296,25 +257,80 @@ def _no_two(grads, masks, out):
         end = max(end, s[1])
 
 
+def _grad_list(torch, grads, masks, out, write):
+    """The C descriptors of a list of gradients, eight 64-bit words each; if they are written, no two may
+    overlap.  (A call on a small model's gradients is bound by this loop, 2 us a tensor.)"""
+    if not isinstance(grads, (list, tuple)):
+        raise TypeError("grads must be a list of tensors")
+    n = len(grads)
+    if masks is not None and len(masks) != n:
+        raise ValueError("masks must hold one entry (a mask or None) per gradient")
+    if out is not None and len(out) != n:
+        raise ValueError("out must hold one tensor per gradient")
+    device, words, spans = grads[0].device, [], []
+    Tensor, f32, bf16, i32 = torch.Tensor, torch.float32, torch.bfloat16, torch.int32
+    for i, g in enumerate(grads):
+        if not isinstance(g, Tensor) or g.device != device:
+            raise TypeError(f"grads[{i}] must be a tensor on {device}")
+        dtype, shape = g.dtype, g.shape
+        if dtype is not f32 and dtype is not bf16:
+            raise TypeError(f"grads[{i}] must be float32 or bfloat16")
+        o = g if out is None else out[i]
+        if o is not g and (not isinstance(o, Tensor) or o.dtype is not dtype or o.shape != shape or o.device != device):
+            raise ValueError(f"out[{i}] must be a tensor like grads[{i}]")
+        m = None if masks is None else masks[i]
+        if m is not None:
+            want = (*shape[:-1], (shape[-1] + 31) // 32) if shape else None
+            if (not isinstance(m, Tensor) or m.dtype is not i32 or m.shape != want or m.device != device
+                    or not m.is_contiguous()):
+                raise ValueError(f"masks[{i}] must be a contiguous int32 tensor of shape {want} on {device}")
+        ptr, flat = g.data_ptr(), g.is_contiguous()
+        to = ptr if o is g else o.data_ptr()
+        if flat and (o is g or o.is_contiguous()):
+            size = g.nbytes
+            if m is None:
+                rows, cols = 1, g.numel()
+            else:
+                cols = shape[-1]
+                rows = g.numel() // cols if cols else 0
+            ld = ldo = cols
+            last, olast = ptr + size, to + size
+        else:
+            if m is None and (o is g or o.stride() == g.stride()):
+                rows, cols, ld = _as_any(g, f"grads[{i}]")
+                ldo = ld
+            else:
+                rows, cols, ld = _as_rows(g, f"grads[{i}]")
+                ldo = ld if o is g else _as_rows(o, f"out[{i}]")[2]
+            last, olast = _last(g), _last(o)
+        words += (ptr, to, 0 if m is None else m.data_ptr(), F32 if dtype is f32 else BF16, rows, cols, ld, ldo)
+        if write and rows and cols:
+            spans.append((to, olast, True, o))
+            if to != ptr:
+                spans.append((ptr, last, False, g))
+            if m is not None:
+                spans.append((words[-6], words[-6] + m.nbytes, False, m))
+    if write:
+        _no_two(spans)
+    return device, words
+
+
 def _clip(torch, grads, masks, out, max_norm):
     if not grads:
         raise ValueError("grads holds no tensor")
     write = max_norm is not None
-    device, words = _grad_list(torch, grads, masks, out)
-    if write:
-        _no_two(grads, masks, out)
+    device, words = _grad_list(torch, grads, masks, out, write)
     n = len(grads)
     table = (ctypes.c_int64 * len(words))(*words)
     size = lib().tsenor_grads_workspace(n)
-    work = torch.empty(size + 8, dtype=torch.uint8, device=device)  # the norm lies behind the partial sums
-    norm = work[size:size + 4].view(torch.float32)[0]
-    head = (ctypes.cast(table, _lib._P), n)
-    tail = (work.data_ptr(), size, norm.data_ptr())
+    work = torch.empty(size // 4 + 1, dtype=torch.float32, device=device)  # the norm lies behind the partial sums
+    start = work.data_ptr()
     if write:
-        _run(torch, "tsenor_clip_grads", device, lib().tsenor_clip_grads, *head, float(max_norm), *tail)
+        _run(torch, "tsenor_clip_grads", device, lib().tsenor_clip_grads, table, n, float(max_norm), start, size,
+             start + size)
     else:
-        _run(torch, "tsenor_grad_norm", device, lib().tsenor_grad_norm, *head, *tail)
-    return norm
+        _run(torch, "tsenor_grad_norm", device, lib().tsenor_grad_norm, table, n, start, size, start + size)
+    return work[size // 4]
 
 
 @_placed

@@ -156,17 +156,20 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
 // a stretch of the reduction, with the loads of kAhead units of 128 bytes in flight; the waves'
 // sums meet in LDS, in wave order.  A lane q = lane / 16 takes bytes 32 q .. 32 q + 31 of a unit of
 // both operands: the two instructions may take the reduction in any order that is the same for both.
-// QX: bf16 tokens become 8-bit integers on the way.  Each workgroup takes the largest
-// magnitudes of all tokens first, while its first weights are loaded.
+// QX: bf16 tokens become 8-bit integers in LDS first, in each workgroup, while its first weights are
+// loaded (as fragments, each lane for itself, 16 lanes would do the same work: 12 us for one token
+// 4096 x 4096, against 7).
 constexpr int kFewWaves = 8;
+constexpr int kFewEntries = kMaxTokenEntries;  // of tokens in LDS, padded rows
 
 template <class T, bool QX, int NT, int MT, class TO>
 __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const GroupedJob job) {
-    constexpr int kAhead = NT * MT >= 4 ? 1 : NT * MT >= 2 ? 2 : 4;
+    constexpr int kAhead = NT * MT >= 4 ? 1 : NT * MT >= 2 ? 2 : 4;  // more registers would leave a CU one workgroup
     typedef typename T::Sum Sum4;
     __shared__ Sum4 sums[kFewWaves][MT * NT][64];
     __shared__ TokenScale scale[QX ? 16 : 1];
     __shared__ uint32_t part[QX ? 16 : 1][kFewWaves];
+    __shared__ u32x4 token[QX ? kFewEntries / 16 + 16 : 1];  // rows of kpad + 16 bytes: no two on the same banks
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t across = (job.inner + 16 * MT - 1) / (16 * MT);
@@ -188,8 +191,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
                   min(inner0 + 16 * m + l16, job.inner - 1) * job.lda + 32 * q;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        brow[n] = static_cast<const uint8_t*>(job.b) + (t.first + (int64_t)min(16 * n + l16, rows - 1)) * job.ldb +
-                  (QX ? 0 : 32 * q);
+        brow[n] = static_cast<const uint8_t*>(job.b) + (t.first + (int64_t)min(16 * n + l16, rows - 1)) * job.ldb + 32 * q;
     Sum4 acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -216,16 +218,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
         }
     };
     if (u0 < u1) load_a(u0);
-    float to_int = 0.f;  // this lane's token
-    int exponent = 0;
+    const int pitch = (int)(job.kbytes / 16) + 1;  // of a token in LDS
     if constexpr (QX) {
-        const int64_t k = job.kbytes;  // entries: one byte of the weights each
+        const int vectors = (int)(job.kbytes / 8);  // of a padded row
+        Eight<uint16_t> first;  // of row 0: all there is of one short token
         for (int r = 0; r < rows; ++r) {
             const uint16_t* x = static_cast<const uint16_t*>(job.b) + (t.first + (int64_t)r) * (job.ldb / 2);
             uint32_t most = 0u;
-            for (int64_t c = 8 * tid; c < k; c += 8 * 64 * kFewWaves) {
+            for (int c = tid; c < vectors; c += 64 * kFewWaves) {
                 Eight<uint16_t> v;
-                v.load(x, c, job.bcols, job.bvec);
+                v.load(x, 8 * c, job.bcols, job.bvec);
+                if (r == 0 && c == tid) first = v;
                 most = max(most, v.magnitude());
             }
             most = max64(most);
@@ -239,9 +242,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
             scale[tid] = token_scale(most);
         }
         __syncthreads();
-        const TokenScale mine = scale[min(l16, rows - 1)];
-        to_int = mine.factor;
-        exponent = mine.exponent;
+        for (int r = 0; r < rows; ++r) {
+            const uint16_t* x = static_cast<const uint16_t*>(job.b) + (t.first + (int64_t)r) * (job.ldb / 2);
+            const TokenScale s = scale[r];
+            for (int c = tid; c < vectors; c += 64 * kFewWaves) {
+                Eight<uint16_t> v = first;
+                if (r > 0 || c != tid) v.load(x, 8 * c, job.bcols, job.bvec);
+                reinterpret_cast<u32x2*>(token + r * pitch)[c] = integers(v, s.factor, s.exponent);
+            }
+        }
+        __syncthreads();
     }
     for (int u = u0; u < u1; u += kAhead) {
         if (u > u0) load_a(u);
@@ -254,13 +264,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if constexpr (QX) {
-                        const int64_t at = 128 * (int64_t)v + 32 * q + 16 * c;  // entry
-                        const uint16_t* x = reinterpret_cast<const uint16_t*>(brow[n]);
-                        Eight<uint16_t> lo, hi;
-                        lo.load(x, at, job.bcols, job.bvec);
-                        hi.load(x, at + 8, job.bcols, job.bvec);
-                        const u32x2 a = integers(lo, to_int, exponent), b = integers(hi, to_int, exponent);
-                        bv[i][n][c] = u32x4{a.x, a.y, b.x, b.y};
+                        bv[i][n][c] = token[min(16 * n + l16, rows - 1) * pitch + 8 * v + 2 * q + c];
                     } else {
                         const uint8_t* p = brow[n] + 128 * (int64_t)v + 16 * c;
                         if (v < whole) __builtin_memcpy(&bv[i][n][c], p, 16);

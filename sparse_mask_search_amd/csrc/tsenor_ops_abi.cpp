@@ -56,12 +56,13 @@ GradJob grad_job(const tsenor_grad& g, bool write) {
     j.bf16 = g.dtype == TSENOR_BF16;
     const bool aligned = !misaligned(g.grad, 16) && (!write || !misaligned(g.out, 16));
     const int64_t per16 = 16 / element_size(g.dtype);
-    if (aligned && j.ld == j.cols && j.ldo == j.cols && (g.mask == nullptr || j.cols >= 8 || j.rows == 1))
+    const bool flat = aligned && j.ld == j.cols && j.ldo == j.cols;
+    if (flat && g.mask == nullptr)
         j.layout = kFlat;
     else if (aligned && j.cols % 8 == 0 && j.ld % per16 == 0 && j.ldo % per16 == 0)
         j.layout = kRows;
     else
-        j.layout = kLoose;
+        j.layout = flat && (j.cols >= 8 || j.rows == 1) ? kFlat : kLoose;
     return j;
 }
 
@@ -206,7 +207,7 @@ int tsenor_gemm_int8(const void* X, int xtype, const float* xscales, int64_t row
     if (experts < 1 || experts > kMaxExperts || (ends == nullptr && experts != 1)) return TSENOR_ERR_PARAM;
     if (rows < 0 || rows >= kMaxRows || m <= 0 || k <= 0 || k > kMaxReduce || ldy < m) return TSENOR_ERR_SHAPE;
     const int64_t kpad = (k + 127) / 128 * 128;
-    if ((ready ? ldx != kpad : ldx < k || rows > 16 || ends != nullptr) || too_big(rows, ldx) || too_big(rows, ldy) ||
+    if ((ready ? ldx != kpad : ldx < k || rows > 16 || rows * kpad > kMaxTokenEntries || ends != nullptr) || too_big(rows, ldx) || too_big(rows, ldy) ||
         too_big(m, kpad) || too_big(experts, m * kpad))
         return TSENOR_ERR_SHAPE;
     if (misaligned(X, ready ? 16 : 2) || misaligned(xscales, 4) || misaligned(A, 16) || misaligned(ascales, 4) ||

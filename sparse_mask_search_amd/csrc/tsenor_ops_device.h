@@ -84,6 +84,23 @@ struct RowTile {
     int first, end;  // rows first .. min(first + tile, end) - 1
 };
 
+// Sum over the lanes up to each one, and each lane's value from the lane before (0 for the first): DPP
+// moves along rows of 16 lanes, then each row's last value into the rows behind.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int from_lane(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, true);
+}
+__device__ __forceinline__ int sum_up_to(int v) {
+    v += from_lane<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+    v += from_lane<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+__device__ __forceinline__ int lane_before(int v) { return from_lane<0x138, 0xF>(v); }  // wave_shr 1
+
 // An entry of `ends` as it counts.
 __device__ __forceinline__ int end_of(const int* ends, int e, int rows) { return min(max(ends[e], 0), rows); }
 
@@ -104,15 +121,10 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
         for (int e0 = 0; e0 < experts; e0 += 64) {
             const int e = e0 + lane;
             const int hi = e < experts ? end_of(ends, e, rows) : 0;
-            int lo = __shfl_up(hi, 1, 64);
+            int lo = lane_before(hi);
             if (lane == 0) lo = last;
             const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
-            int sum = n;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(sum, d, 64);
-                if (lane >= d) sum += o;
-            }
+            const int sum = sum_up_to(n);
             const uint64_t behind = __ballot(t >= 0 && before + sum > t);
             if (behind != 0) {
                 const int l = __builtin_ctzll(behind);
@@ -146,7 +158,7 @@ __device__ __forceinline__ void expert_rows(const int* ends, int experts, int ro
     for (int e = threadIdx.x; e < experts; e += blockDim.x) table.end[e] = end_of(ends, e, rows);
     if (experts > 64) return;
     const int lane = threadIdx.x & 63;
-    const int hi = lane < experts ? end_of(ends, lane, rows) : 0, lo = __shfl_up(hi, 1, 64);
+    const int hi = lane < experts ? end_of(ends, lane, rows) : 0, lo = lane_before(hi);
     const int n = lane < experts ? hi - (lane == 0 ? 0 : lo) : 0;
     int rank = 0;
     for (int e = 0; e < experts; ++e) {
@@ -167,15 +179,10 @@ __device__ __forceinline__ int row_table(const int* ends, int experts, int rows,
     for (int e0 = 0; e0 < experts; e0 += 64) {
         const int e = e0 + lane;
         const int hi = e >= experts ? 0 : ends == nullptr ? rows : end_of(ends, e, rows);
-        int lo = __shfl_up(hi, 1, 64);
+        int lo = lane_before(hi);
         if (lane == 0) lo = last;
         const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += o;
-        }
+        const int sum = sum_up_to(n);
         if (e < experts && threadIdx.x < 64) {
             table.tile[e] = before + sum - n;
             table.row[e] = lo;

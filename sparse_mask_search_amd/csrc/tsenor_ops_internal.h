@@ -34,6 +34,7 @@ int launch_grouped_wgrad(const GroupedJob& job, bool bf16out, void* stream);
 
 int launch_quant_int8(const void* X, int bf16, int64_t batch, int64_t stride, int64_t rows, int64_t cols,
                       int64_t ldx, int8_t* values, float* scales, void* stream);
+constexpr int kMaxTokenEntries = 32768;  // bf16 tokens that are quantised on the way, padded
 // bf16x: job.b holds bf16 tokens (at most 16), quantised on the way
 int launch_gemm_int8(const GroupedJob& job, bool bf16x, bool bf16out, void* stream);
 

@@ -164,14 +164,38 @@ def test_lists_that_overlap_are_found():
     from sparse_mask_search_amd import _ops
     buf = torch.zeros(8, 64)
     a, b = buf[:, :32], buf[:, 32:]
-    _ops._no_two([a, b], None, None)
-    _ops._no_two([buf[:4], buf[4:]], None, None)
-    _ops._no_two([buf[:4]], None, [buf[4:]])
-    _ops._no_two([a.t(), b.t()], None, None)
-    _ops._no_two([buf[:0], buf], None, None)
+
+    def check(grads, masks=None, out=None):
+        _ops._grad_list(torch, grads, masks, out, True)
+    words = buf.view(torch.int32)
+    check([a, b])
+    check([buf[:4], buf[4:]])
+    check([buf[:4]], [words[4:6].view(-1)[:8].view(4, 2)])
+    check([a.t(), b.t()])
+    check([buf[:0], buf])
+    check([buf[:2]], out=[buf[2:4]])
+    check([a[:4], b[:4]], out=[a[4:], b[4:]])
+    _ops._grad_list(torch, [buf, buf], None, None, False)  # a norm writes nothing
     for grads, masks, out in (([buf, buf], None, None), ([a, buf[:, 31:40]], None, None), ([buf[:5], buf[4:]], None, None),
                               ([buf[:4]], None, [buf[2:6]]), ([buf[:2], buf[2:4]], None, [buf[4:6], buf[5:7]]),
                               ([buf[:2], buf[2:4]], None, [buf[4:6], buf[:2]]),
-                              ([buf], [buf.view(torch.int32)[:, :2]], None)):
+                              ([buf[:4]], [words[1:2].view(-1)[:8].view(4, 2)], None)):
         with pytest.raises(ValueError, match="overlaps"):
-            _ops._no_two(grads, masks, out)
+            check(grads, masks, out)
+
+
+def test_gradients_that_do_not_fit_are_refused():
+    from sparse_mask_search_amd import _ops
+    g, m = torch.zeros(4, 40), torch.zeros(4, 2, dtype=torch.int32)
+    ok = ([g], [m], [torch.zeros(4, 40)])
+    _ops._grad_list(torch, *ok, True)
+    for change, match in ((dict(grads=[g.double()]), "grads"), (dict(masks=[m, m]), "masks"), (dict(masks=[m.long()]), "masks"),
+                          (dict(masks=[m[:, :1]]), "masks"), (dict(masks=[m[:2]]), "masks"), (dict(out=[]), "out"),
+                          (dict(out=[g[:2]]), "out"), (dict(out=[torch.zeros(4, 40, dtype=torch.bfloat16)]), "out"),
+                          (dict(grads=[torch.zeros(4, 4, 80)[..., ::2]], masks=None, out=None), "grads"),
+                          (dict(grads=[torch.zeros(40, 4).t()], out=None), "grads"), (dict(grads=(x for x in [g])), "grads"),
+                          (dict(grads=[torch.zeros(())], masks=[m], out=None), "masks"), (dict(grads=[None]), "")):
+        args = dict(grads=[g], masks=[m], out=None)
+        args.update(change)
+        with pytest.raises((TypeError, ValueError, AttributeError), match=match):
+            _ops._grad_list(torch, args["grads"], args["masks"], args["out"], True)
