@@ -405,14 +405,16 @@ __device__ __forceinline__ void put_last(V* to, V v) {
 }
 
 // The results of a wave's FA x FB tiles of 16 x 16, rows row0 + STEP j, columns c0 + 16 i + 4 q (c0 a
-// multiple of 32).  Where all rows and columns exist, what scales or masks them is loaded first (a load among the
-// stores would wait for all of those before it), and bf16 results of two neighbouring tiles change
-// places between the lane quarters, so that a store has 16 bytes.
-template <class T, Kind K, int FA, int FB, int STEP, class TO>
+// multiple of 32).  Where all rows and columns exist, what scales them is loaded first (a load among the
+// stores would wait for all of those before it), mask words come from LDS (`words`, kWords a row) if they are
+// there, and bf16 results of two neighbouring tiles change places between the lane quarters, so that a
+// store has 16 bytes.
+template <class T, Kind K, int FA, int FB, int STEP, int kWords, class TO>
 __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, int row0, bool complete, int rows, int c0,
-                                           int q, const typename T::Sum* sums, TO* out) {
+                                           int q, const typename T::Sum* sums, const uint32_t* words, TO* out) {
     constexpr bool kScaled = T::kSize == 1, kMasked = K == kGradient, kHalf = sizeof(TO) == 2;
-    if (!complete || c0 + 16 * FA > (int)job.inner || !(kHalf ? job.ovec8 : job.ovec)) {
+    const bool elsewhere = kMasked && job.mask != nullptr && words == nullptr;
+    if (!complete || elsewhere || c0 + 16 * FA > (int)job.inner || !(kHalf ? job.ovec8 : job.ovec)) {
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
             const int row = row0 + STEP * j;
@@ -427,7 +429,6 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
     }
     f32x4 across[kScaled ? FA : 1];
     float down[kScaled ? FB : 1];
-    uint32_t keep[kMasked ? FB : 1][kMasked ? FA / 2 : 1];
     if constexpr (kScaled) {
         const float* as = job.as + expert * job.inner + c0 + 4 * q;
 #pragma unroll
@@ -437,21 +438,15 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
 #pragma unroll
         for (int j = 0; j < FB; ++j) down[j] = job.bs[row0 + STEP * j];
     }
-    if constexpr (kMasked) {
-        const int64_t words = (job.inner + 31) / 32;
-#pragma unroll
-        for (int j = 0; j < FB; ++j) {
-            const uint32_t* row = job.mask + (expert * job.outer + row0 + STEP * j) * words + (c0 >> 5);
-#pragma unroll
-            for (int i = 0; i < FA / 2; ++i) keep[j][i] = job.mask == nullptr ? 0xFFFFFFFFu : row[i];
-        }
-    }
     TO* y = out + row0 * job.ldo + c0 + (kHalf ? 16 * (q & 1) + 8 * (q >> 1) : 4 * q);
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
 #pragma unroll
         for (int i = 0; i < FA; i += 2) {
             __builtin_amdgcn_sched_barrier(0);
+            uint32_t keep = 0xFFFFFFFFu;
+            if constexpr (kMasked)
+                if (words != nullptr) keep = words[STEP * j * kWords + i / 2];
             f32x4 v[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p)
@@ -459,7 +454,7 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
                 for (int e = 0; e < 4; ++e) {
                     float x = (float)sums[(i + p) * FB + j][e];
                     if constexpr (kScaled) x = x * down[j] * across[i + p][e];
-                    if constexpr (kMasked) x = (keep[j][i / 2] >> (16 * p + 4 * q + e)) & 1u ? x : 0.f;
+                    if constexpr (kMasked) x = (keep >> (16 * p + 4 * q + e)) & 1u ? x : 0.f;
                     v[p][e] = x;
                 }
             if constexpr (kHalf) {
@@ -499,6 +494,10 @@ struct AtEnd {
     static constexpr bool value = true;
 };
 template <int N>
+struct MaskWords {
+    uint32_t word[N];
+};
+template <int N>
 struct Count {
     static constexpr int value = N;
 };
@@ -508,6 +507,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
     constexpr int W = WM * WN, TA = TM / WM / 32, TB = TN / WN / 32;
     typedef Loads<T, AT, TM, W> LoadsA;
     typedef Loads<T, BT, TN, W> LoadsB;
+    constexpr bool kMasked = K == kGradient && LONG;
     static_assert(DIRECT ? R >= 4 : R == 3 && !AT && !BT, "ring");
     struct Buffer {
         u32x4 a[TM * 4];
@@ -519,6 +519,14 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
     const int wm = wave / WN, wn = wave % WN;
     const int across = (int)((job.inner + TM - 1) / TM);
     const int down = K == kGradient ? (int)((job.outer + TN - 1) / TN) : 0;  // of one expert
+
+    // The mask words of a weight gradient's tile come by direct loads too, before its first step: they have
+    // landed when its results are written.  Two sets in turn, since other waves may still be at
+    // the tile before.
+    constexpr int kWords = TM / 32, kMaskLoads = kMasked ? TN * kWords / 64 / W : 0;
+    static_assert(kMaskLoads * 64 * W == (kMasked ? TN * kWords : 0), "mask words");
+    uint32_t* words = nullptr;
+    if constexpr (kMasked) words = lds<MaskWords<2 * TN * kWords>>().word;
 
     struct Tile {  // the same in all lanes, but for the loads' offsets
         int expert, inner0, outer0, outer_end, full, steps;
@@ -636,6 +644,19 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         if (j < LoadsA::kCount) LoadsA::store(buf.a, j, held[set][j], wave, lane);
         else LoadsB::store(buf.b, j - LoadsA::kCount, held[set][j], wave, lane);
     };
+    int set = 0;  // of mask words
+    const auto load_words = [&]() __attribute__((always_inline)) {
+        const int64_t wpr = (job.inner + 31) / 32;
+        const uint8_t* first = uniform(reinterpret_cast<const uint8_t*>(
+            job.mask + (cur.expert * job.outer + cur.outer0) * wpr + cur.inner0 / 32));
+        const int rows = min(cur.outer_end - cur.outer0, TN), have = min((int)wpr - cur.inner0 / 32, kWords);
+#pragma unroll
+        for (int j = 0; j < kMaskLoads; ++j) {
+            const int slot = 64 * (wave * kMaskLoads + j) + lane;
+            dma4(first, 4 * (__umul24(min(slot / kWords, rows - 1), (uint32_t)wpr) + min(slot % kWords, have - 1)),
+                 lds_offset(words + TN * kWords * set + 64 * (wave * kMaskLoads + j)));
+        }
+    };
     typename T::Sum acc[TA][2][TB][2];  // pairs of 16: tiles of 32 x 32
     u32x4 fa[2][2], fb[2][TB][2];
     const auto read_a = [&](int i, const Buffer& buf) __attribute__((always_inline)) {  // into the set i & 1
@@ -735,6 +756,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         for (int i = 0; i < 2 * TA; ++i)
 #pragma unroll
             for (int j = 0; j < 2 * TB; ++j) acc[i >> 1][i & 1][j >> 1][j & 1] = typename T::Sum{0, 0, 0, 0};
+        if constexpr (kMasked) {
+            set ^= 1;
+            if (job.mask != nullptr) load_words();
+        }
         int t = 0;
         const auto two_steps = [&](auto end, auto pairs) __attribute__((always_inline)) {
             const int one = inc(at), two = inc(one), last = dec(at);
@@ -751,8 +776,11 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         if (K == kProduct && TB > 1 && cur.outer_end - cur.outer0 <= TN / 2) all_steps(Count<TB / 2 + (TB == 1)>());
         else all_steps(Count<TB>());
         const int row0 = cur.outer0 + 16 * wn + (lane & 15), c0 = cur.inner0 + (TM / WM) * wm;
-        store_tile<T, K, 2 * TA, 2 * TB, 16 * WN>(
-            job, cur.expert, row0, cur.outer_end - cur.outer0 >= TN, cur.outer_end, c0, lane >> 4, &acc[0][0][0][0],
+        const uint32_t* kept =
+            kMasked && job.mask != nullptr ? words + TN * kWords * set + (16 * wn + (lane & 15)) * kWords + TM / WM / 32 * wm
+                                           : nullptr;
+        store_tile<T, K, 2 * TA, 2 * TB, 16 * WN, kWords>(
+            job, cur.expert, row0, cur.outer_end - cur.outer0 >= TN, cur.outer_end, c0, lane >> 4, &acc[0][0][0][0], kept,
             static_cast<TO*>(job.out) + (K == kGradient ? cur.expert * job.ostride : 0));
         if (!more) break;
         cur = nxt;
@@ -842,7 +870,7 @@ int product(const GroupedJob& job, void* stream) {
         if (job.rows <= 64 && tiles_of<K>(job, 64, 64) < 128) return few<T, false, 2, 2, TO>(job, stream);
     }
     // tiles count rows, columns and the bytes between rows in 32 bits
-    if (job.inner > 0x7FFFFF00 || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow || job.ldb >= kMaxRow)
+    if (job.inner > (K == kGradient ? 1 << 26 : 0x7FFFFF00) || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow || job.ldb >= kMaxRow)
         return any<T, AT, BT, K, TO>(job, stream);
     const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
     if (!direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) ||

@@ -194,7 +194,7 @@ def test_gradients_that_do_not_fit_are_refused():
                           (dict(out=[g[:2]]), "out"), (dict(out=[torch.zeros(4, 40, dtype=torch.bfloat16)]), "out"),
                           (dict(grads=[torch.zeros(4, 4, 80)[..., ::2]], masks=None, out=None), "grads"),
                           (dict(grads=[torch.zeros(40, 4).t()], out=None), "grads"), (dict(grads=(x for x in [g])), "grads"),
-                          (dict(grads=[torch.zeros(())], masks=[m], out=None), "masks"), (dict(grads=[None]), "")):
+                          (dict(grads=[torch.zeros(())], masks=[m], out=None), "masks"), (dict(grads=[None]), "device")):
         args = dict(grads=[g], masks=[m], out=None)
         args.update(change)
         with pytest.raises((TypeError, ValueError, AttributeError), match=match):
