@@ -19,18 +19,24 @@ using namespace ops;
 
 enum Kind { kProduct, kGradient };
 
-// Sixteen bytes of a row of which `valid` are there, at any alignment of the entries; zeros
-// behind them.
+// Sixteen bytes at any alignment of the entries.  (Global loads by name: a pointer that the compiler
+// cannot place makes it a flat load, which waits for LDS too.)
+typedef u32x4 __attribute__((aligned(1), may_alias)) any16;
+typedef __attribute__((address_space(1))) const uint8_t global_byte;
+__device__ __forceinline__ u32x4 load16(const uint8_t* p) {
+    return *(__attribute__((address_space(1))) const any16*)(global_byte*)p;
+}
+// The same of which `valid` are there; zeros behind them.
 template <class T>
 __device__ __forceinline__ u32x4 load16(const uint8_t* p, int64_t valid) {
+    if (valid >= 16) return load16(p);
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (valid >= 16) {
-        __builtin_memcpy(&v, p, 16);
-    } else if (valid > 0) {
+    if (valid > 0) {
 #pragma unroll
         for (int i = 0; i < 16 / T::kSize; ++i)
             if (i * T::kSize < valid) {
-                const uint32_t x = T::kSize == 2 ? reinterpret_cast<const uint16_t*>(p)[i] : p[i];
+                const uint32_t x = T::kSize == 2 ? ((__attribute__((address_space(1))) const uint16_t*)(global_byte*)p)[i]
+                                                 : ((global_byte*)p)[i];
                 v[i * T::kSize / 4] |= x << (8 * (i * T::kSize % 4));
             }
     }
@@ -211,7 +217,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
                 const uint8_t* p = arow[m] + 128 * (int64_t)v;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (v < whole) __builtin_memcpy(&av[i][m][c], p + 16 * c, 16);
+                    if (v < whole) av[i][m][c] = load16(p + 16 * c);
                     else av[i][m][c] = load16<T>(p + 16 * c, job.kbytes - 128 * (int64_t)v - 32 * q - 16 * c);
                 }
             }
@@ -267,7 +273,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
                         bv[i][n][c] = token[min(16 * n + l16, rows - 1) * pitch + 8 * v + 2 * q + c];
                     } else {
                         const uint8_t* p = brow[n] + 128 * (int64_t)v + 16 * c;
-                        if (v < whole) __builtin_memcpy(&bv[i][n][c], p, 16);
+                        if (v < whole) bv[i][n][c] = load16(p);
                         else bv[i][n][c] = load16<T>(p, job.kbytes - 128 * (int64_t)v - 32 * q - 16 * c);
                     }
                 }
@@ -379,11 +385,7 @@ struct Loads {
     __device__ static __forceinline__ u32x4 fetch(const Loads& of, bool inside, int j, int64_t s, int64_t reduce, int wave,
                                                   int lane) {
         const uint8_t* p = of.base + s * of.step + of.offset[j];
-        if (inside) {
-            u32x4 v;
-            __builtin_memcpy(&v, p, 16);
-            return v;
-        }
+        if (inside) return load16(p);
         const int slot = 64 * (wave * kCount + j) + lane, r = slot / 4;
         return load16<T>(p, reduce - 64 * s - 16 * (row_slot(r, slot % 4) - 4 * r));
     }
@@ -407,8 +409,7 @@ __device__ __forceinline__ void put_last(V* to, V v) {
 // The results of a wave's FA x FB tiles of 16 x 16, rows row0 + STEP j, columns c0 + 16 i + 4 q (c0 a
 // multiple of 32).  Where all rows and columns exist, what scales them is loaded first (a load among the
 // stores would wait for all of those before it), mask words come from LDS (`words`, kWords a row) if they are
-// there, and bf16 results of two neighbouring tiles change places between the lane quarters, so that a
-// store has 16 bytes.
+// there, and a store writes 16 bytes a lane.
 template <class T, Kind K, int FA, int FB, int STEP, int kWords, class TO>
 __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, int row0, bool complete, int rows, int c0,
                                            int q, const typename T::Sum* sums, const uint32_t* words, TO* out) {
@@ -438,34 +439,58 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
 #pragma unroll
         for (int j = 0; j < FB; ++j) down[j] = job.bs[row0 + STEP * j];
     }
-    TO* y = out + row0 * job.ldo + c0 + (kHalf ? 16 * (q & 1) + 8 * (q >> 1) : 4 * q);
+    // Sixteen bytes of a lane's row, from one (fp32) or two neighbouring tiles (bf16: they change
+    // places between the lane quarters): 64 bytes of each of 16 rows.
+    const auto piece = [&](int i, int j) __attribute__((always_inline)) {
+        uint32_t keep = 0xFFFFFFFFu;
+        if constexpr (kMasked)
+            if (words != nullptr) keep = words[STEP * j * kWords + i / 2];
+        f32x4 v[kHalf ? 2 : 1];
+#pragma unroll
+        for (int p = 0; p < (kHalf ? 2 : 1); ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = (float)sums[(i + p) * FB + j][e];
+                if constexpr (kScaled) x = x * down[j] * across[i + p][e];
+                if constexpr (kMasked) x = (keep >> (16 * ((i + p) & 1) + 4 * q + e)) & 1u ? x : 0.f;
+                v[p][e] = x;
+            }
+        if constexpr (kHalf) {
+            const u32x2 lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[1][0], v[1][1]),
+                                                              false, false);
+            const u32x2 hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][2], v[0][3]), pack_bf16(v[1][2], v[1][3]),
+                                                              false, false);
+            return u32x4{lo.x, hi.x, lo.y, hi.y};
+        } else {
+            return __builtin_bit_cast(u32x4, v[0]);
+        }
+    };
+    constexpr int kPiece = kHalf ? 2 : 1;         // tiles of one
+    // Two pieces to each store, whole lines of 8 rows, for weight gradients: 1022 rows of 16 experts 1792 x
+    // 7680 in fp32 298 -> 178 us (5.1 TB/s), 8192 rows of 16 2048 x 4096 216 -> 193, in bf16 164 -> 161.  Products, whose
+    // results are a smaller part, gain nothing.
+    constexpr bool kLines = K == kGradient && FA % (2 * kPiece) == 0;
+    const int l16 = threadIdx.x & 15, col = kHalf ? 16 * (q & 1) + 8 * (q >> 1) : 4 * q;
+    TO* y = out + (kLines ? row0 - (l16 & 8) : row0) * job.ldo + c0 + col + (kLines ? (l16 >> 3) * 16 * kPiece : 0);
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
 #pragma unroll
-        for (int i = 0; i < FA; i += 2) {
+        for (int i = 0; i < FA; i += (kLines ? 2 : 1) * kPiece) {
             __builtin_amdgcn_sched_barrier(0);
-            uint32_t keep = 0xFFFFFFFFu;
-            if constexpr (kMasked)
-                if (words != nullptr) keep = words[STEP * j * kWords + i / 2];
-            f32x4 v[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
+            const u32x4 a = piece(i, j);
+            if constexpr (kLines) {
+                // lanes 8 .. 15 of 16 take the second piece of the first eight rows, and give their first piece
+                const u32x4 b = piece(i + kPiece, j);
+                u32x4 upper, lower;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x = (float)sums[(i + p) * FB + j][e];
-                    if constexpr (kScaled) x = x * down[j] * across[i + p][e];
-                    if constexpr (kMasked) x = (keep >> (16 * p + 4 * q + e)) & 1u ? x : 0.f;
-                    v[p][e] = x;
+                    upper[e] = (uint32_t)__builtin_amdgcn_update_dpp((int)a[e], (int)b[e], 0x128, 0xF, 0xC, false);
+                    lower[e] = (uint32_t)__builtin_amdgcn_update_dpp((int)b[e], (int)a[e], 0x128, 0xF, 0x3, false);
                 }
-            if constexpr (kHalf) {
-                const u32x2 lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][0], v[0][1]),
-                                                                  pack_bf16(v[1][0], v[1][1]), false, false);
-                const u32x2 hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0][2], v[0][3]),
-                                                                  pack_bf16(v[1][2], v[1][3]), false, false);
-                put_last<K>(reinterpret_cast<u32x4*>(y + 16 * i), u32x4{lo.x, hi.x, lo.y, hi.y});
+                put_last<K>(reinterpret_cast<u32x4*>(y + 16 * i), upper);
+                put_last<K>(reinterpret_cast<u32x4*>(y + 8 * job.ldo + 16 * i), lower);
             } else {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) put_last<K>(reinterpret_cast<f32x4*>(y + 16 * (i + p)), v[p]);
+                put_last<K>(reinterpret_cast<u32x4*>(y + 16 * i), a);
             }
         }
         y += STEP * job.ldo;
@@ -869,16 +894,22 @@ int product(const GroupedJob& job, void* stream) {
         }
         if (job.rows <= 64 && tiles_of<K>(job, 64, 64) < 128) return few<T, false, 2, 2, TO>(job, stream);
     }
-    // tiles count rows, columns and the bytes between rows in 32 bits
-    if (job.inner > (K == kGradient ? 1 << 26 : 0x7FFFFF00) || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow || job.ldb >= kMaxRow)
-        return any<T, AT, BT, K, TO>(job, stream);
-    const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
-    if (!direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) ||
-        !direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes)) {
-        // 16384 rows of 8 experts 11009 x 4095: 5855 us in tiles of 64 x 64, 3613 in tiles of 256 x 128
-        if constexpr (!AT && !BT)
-            if (tiles_of<K>(job, 256, 128) >= 160) return tile<T, AT, BT, K, 256, 128, 2, 4, 3, true, false, TO>(job, stream);
-        return any<T, AT, BT, K, TO>(job, stream);
+    if constexpr (T::kSize == 2) {  // 8-bit integers are aligned, and their rows short
+        // tiles count rows, columns and the bytes between rows in 32 bits
+        if (job.inner > (K == kGradient ? 1 << 26 : 0x7FFFFF00) || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow ||
+            job.ldb >= kMaxRow)
+            return any<T, AT, BT, K, TO>(job, stream);
+        const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
+        if (!direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) ||
+            !direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes)) {
+            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5850 / 3200; 1003 rows of 16
+            // experts 2047 x 4095: 132 / 157; column-contiguous operands, 8192 rows of 16 experts 4095 x 2047: 764 / 829,
+            // weight gradients 739 / 800.
+            if constexpr (!AT && !BT)
+                if (tiles_of<K>(job, 256, 128) >= 160)
+                    return tile<T, AT, BT, K, 256, 128, 2, 4, 3, true, false, TO>(job, stream);
+            return any<T, AT, BT, K, TO>(job, stream);
+        }
     }
     const int variant = pick_tile<K>(job);
     if (variant == 0) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, true, TO>(job, stream);
