@@ -199,12 +199,16 @@ def gemm_int8(torch, X, A, ends=None, out=None, dtype=None):
     yt = _float_type(torch, out, "out")
     if rows == 0 or m == 0:
         return out
-    if not ready and xt == BF16 and ends is None and rows <= 16 and rows * _pad(k) <= 32768:
-        x, xtype, xs, ldx = X, BF16, None, _ld(X)
-    else:
-        q = X if ready else _quantised(torch, X)
-        x, xtype, xs, ldx = q.values, INT8, q.scales.data_ptr(), q.values.shape[1]
-    _run(torch, "tsenor_gemm_int8", device, lib().tsenor_gemm_int8, x.data_ptr(), xtype, xs, rows, ldx,
+    if ready:
+        x, xtype, xs, ldx = X.values.data_ptr(), INT8, X.scales.data_ptr(), X.values.shape[1]
+    elif xt == BF16 and ends is None and rows <= 16 and rows * _pad(k) <= 32768:
+        x, xtype, xs, ldx = X.data_ptr(), BF16, None, _ld(X)
+    else:  # quantised into one buffer, scales behind the values
+        ldx = _pad(k)
+        q = torch.empty(rows * (ldx + 4), dtype=torch.int8, device=device)
+        x, xtype, xs = q.data_ptr(), INT8, q.data_ptr() + rows * ldx
+        _run(torch, "tsenor_quant_int8", device, lib().tsenor_quant_int8, X.data_ptr(), xt, 1, 0, rows, k, _ld(X), x, xs)
+    _run(torch, "tsenor_gemm_int8", device, lib().tsenor_gemm_int8, x, xtype, xs, rows, ldx,
          A.values.data_ptr(), A.scales.data_ptr(), experts, m, k, None if ends is None else ends.data_ptr(),
          out.data_ptr(), yt, _ld(out))
     return out

@@ -844,11 +844,12 @@ bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0;
 }
 
+// Tiles of a launch, as far as the host can know: a little more than half a tile counted for each expert.
 template <Kind K>
-int64_t tiles_of(const GroupedJob& job, int64_t m, int64_t n) {  // half a tile more counted for each expert
+int64_t tiles_of(const GroupedJob& job, int64_t m, int64_t n) {
     const int64_t across = (job.inner + m - 1) / m;
     return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
-                                    : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts / 2 : 0));
+                                    : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts * 9 / 16 : 0));
 }
 
 template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, bool DIRECT, class TO>
@@ -864,18 +865,34 @@ int tile(const GroupedJob& job, void* stream) {
     return (int)hipGetLastError();
 }
 
-// Tiles: 0: 256 x 256; 1: 256 x 128, a ring of six; 2: 64 x 64, a ring of eight; 3: 64 x 64, four.  The
-// larger ones need about 160 workgroups (half a tile more counted for each expert); 2 is for experts with
-// few rows, where reading the weights bounds.  Measured (us) for 0 / 1 / 2 / 3: 16384 rows of 8 experts
-// 11008 x 4096: 1252 / 1645 / 3972 / 3152; 4096 rows of 16 experts 2048 x 4096 (192 tiles of 256 x 256): 116 / 153 /
-// 203 / 198; 2048 rows (192 of 256 x 128): 111 / 94 / 130 / 133; 1003 rows: 101 / 93 / 83 / 90; 100 rows: 82 /
-// 77 / 60 / 64; 512 rows 4096 x 4096: 74 / 53 / 38 / 35; weight gradients, 2048 rows of 8 experts 1024 x 2048 (256
-// tiles): 23 / 25 / 43 / 29; 1001 rows of 4 experts 1024 x 1024: 21 / 15 / 13 / 11.
+// The tile whose rounds of workgroups take the least time.  Measured, hundredths of a microsecond for a step
+// (64 bytes of the reduction) of one round: 256 x 256: 60; 256 x 128: 43; 128 x 128: 31; 64 x 64: 19 with one
+// workgroup on a CU, 28 with two (weight gradients: 27 and, with four, 50).  Examples (us), in that order: 1542 rows
+// 2048 x 5952 102 / 77 / 55 / 94; 600 rows 8192 x 4096 76 / 56 / 70 / 84; 600 rows of 16 experts 2048 x 4096
+// 95 / 89 / 67 / 77; 2048 rows of them 111 / 94 / 102 / 130; 4096 rows 116 / 153 / 146 / 203; data gradients, 200 rows of
+// 8 experts 2048 x 4096 62 / 55 / 40 / 27; 16384 rows of 8 experts 11008 x 4096 1252 / 1645 / 2047 / 3972; weight
+// gradients, 8192 rows 2048 x 2048 164 / - / 86 / 127, 1001 rows of 4 experts 1024 x 1024 21 / - / 12 / 10.
+enum Tile { k256x256, k256x128, k128x128, k64x64 };
 template <Kind K>
-int pick_tile(const GroupedJob& job) {
-    if (tiles_of<K>(job, 256, 256) >= 160) return 0;
-    if (K == kProduct && tiles_of<K>(job, 256, 128) >= 160) return 1;
-    return K == kProduct && job.rows <= 64 * (int64_t)job.experts ? 2 : 3;
+Tile pick_tile(const GroupedJob& job) {
+    const auto rounds = [&](int64_t m, int64_t n, int64_t at_once) {
+        return (tiles_of<K>(job, m, n) + at_once - 1) / at_once;
+    };
+    Tile best = k256x256;
+    int64_t least = 60 * rounds(256, 256, kCus);
+    const auto take = [&](Tile tile, int64_t cost) {
+        if (cost < least) {
+            best = tile;
+            least = cost;
+        }
+    };
+    if (K == kProduct) take(k256x128, 43 * rounds(256, 128, kCus));
+    take(k128x128, 31 * rounds(128, 128, kCus));
+    const int64_t small = tiles_of<K>(job, 64, 64);
+    if (small <= kCus) take(k64x64, K == kProduct ? 19 : 27);
+    else if (K == kGradient) take(k64x64, 50 * rounds(64, 64, 4 * kCus));
+    else take(k64x64, std::max<int64_t>(28, 28 * small / (2 * kCus)));  // these do not go in rounds
+    return best;
 }
 
 template <class T, bool AT, bool BT, Kind K, class TO>
@@ -911,13 +928,15 @@ int product(const GroupedJob& job, void* stream) {
             return any<T, AT, BT, K, TO>(job, stream);
         }
     }
-    const int variant = pick_tile<K>(job);
-    if (variant == 0) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, true, TO>(job, stream);
+    const Tile variant = pick_tile<K>(job);
+    if (variant == k256x256) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, true, TO>(job, stream);
+    if (variant == k128x128) return tile<T, AT, BT, K, 128, 128, 2, 4, 8, true, true, TO>(job, stream);
     if constexpr (K == kProduct) {
-        if (variant == 1) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, true, TO>(job, stream);
-        if (variant == 2) return tile<T, AT, BT, K, 64, 64, 2, 2, 8, true, true, TO>(job, stream);
+        if (variant == k256x128) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, true, TO>(job, stream);
+        return tile<T, AT, BT, K, 64, 64, 2, 2, 8, true, true, TO>(job, stream);
+    } else {
+        return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, true, TO>(job, stream);
     }
-    return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, true, TO>(job, stream);
 }
 
 }  // namespace
