@@ -12,8 +12,8 @@
  * int32 [experts]) holds for each expert the row behind its last one: expert e
  * owns rows ends[e-1] .. ends[e]-1 (from 0 for e = 0), which may be none.  Rows
  * from ends[experts-1] on belong to no expert; their results are zeros.  The
- * host never reads `ends`: entries below 0 count as 0, above `rows` as `rows`;
- * if they descend, which product a row gets is unspecified (memory-safe).
+ * host never reads `ends`: entries below 0 count as 0, above `rows` as `rows`,
+ * and one below an earlier one as that one.
  *
  * 8-bit integer operands [rows][k]: values int8 [rows][kpad], kpad = k rounded up
  * to a multiple of 128, the entries behind k zeros; scales fp32 [rows].  A row
@@ -52,8 +52,8 @@ enum { TSENOR_INT8 = 3 };
  *   X      bf16 [rows][ldx], ldx >= k;  W  bf16, expert e at W + e * stride;
  *   Y      ytype f32 or bf16, [rows][ldy], ldy >= m.
  * rows == 0 is a no-op.  Errors: _NULL, _DTYPE, _PARAM (transpose not 0 or 1,
- * experts < 1 or > 1024), _SHAPE (rows < 0 or >= 2^31, m, k <= 0, leading
- * dimensions, stride, alignment).                                             */
+ * experts < 1 or > 1024), _SHAPE (rows < 0 or >= 2^30, m, k <= 0, k >= 2^30,
+ * leading dimensions, stride, alignment).                                     */
 int tsenor_grouped_mm(const uint16_t* X, int64_t rows, int64_t ldx, const uint16_t* W,
                       int transpose, int64_t experts, int64_t stride, int64_t ldw, int64_t m,
                       int64_t k, const int* ends, void* Y, int ytype, int64_t ldy, void* stream);
@@ -90,7 +90,7 @@ int tsenor_quant_int8(const void* X, int dtype, int64_t batch, int64_t stride, i
  *   ends   as above, or NULL: one weight (experts 1) for all rows;
  *   Y      ytype f32 or bf16, [rows][ldy], ldy >= m.
  * rows == 0 is a no-op.  Errors: _NULL, _DTYPE, _PARAM (experts < 1 or > 1024,
- * experts != 1 without ends), _SHAPE (rows < 0 or >= 2^31, m, k <= 0, k > 2^17,
+ * experts != 1 without ends), _SHAPE (rows < 0 or >= 2^30, m, k <= 0, k > 2^17,
  * leading dimensions, more rows than allowed for bf16, alignment: values 16 bytes). */
 int tsenor_gemm_int8(const void* X, int xtype, const float* xscales, int64_t rows, int64_t ldx,
                      const int8_t* A, const float* ascales, int64_t experts, int64_t m, int64_t k,

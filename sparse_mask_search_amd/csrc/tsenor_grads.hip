@@ -119,7 +119,8 @@ __device__ __forceinline__ void chunk(const GradJob& g, int64_t begin, float f, 
         const float inv = 1.f / (float)per;
         const T* from = x + row0 * g.ld;
         T* to = y + row0 * g.ldo;
-        const uint8_t* keep = reinterpret_cast<const uint8_t*>(g.mask + row0 * words);  // a byte a vector
+        const uint8_t* keep =  // a byte a vector
+            g.mask == nullptr ? nullptr : reinterpret_cast<const uint8_t*>(g.mask + row0 * words);
         Eight<T> v[kUnroll];
         Vector p[kUnroll];
         uint32_t bits[kUnroll];

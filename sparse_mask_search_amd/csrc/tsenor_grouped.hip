@@ -101,8 +101,9 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
         expert = (int)(t / down);
         outer0 = t % down * 64;
         outer_end = job.outer;
-        const int first = expert == 0 ? 0 : end_of(job.ends, expert - 1, job.rows);
-        count = max(end_of(job.ends, expert, job.rows) - first, 0);
+        int first, end;
+        rows_of(job.ends, job.rows, expert, &first, &end);
+        count = end - first;
         a += first * job.lda + inner0 * T::kSize;
         b += first * job.ldb + outer0 * T::kSize;
         out += expert * job.ostride;
@@ -113,7 +114,8 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
 
     auto fetch = [&](const uint8_t* base, int64_t ld, int64_t have, bool turned, int s) {
         if (!turned) {
-            const int r = tid >> 2, c = 64 * s + 16 * (tid & 3);
+            const int r = tid >> 2;
+            const int64_t c = 64 * (int64_t)s + 16 * (tid & 3);
             return load16<T>(base + min((int64_t)r, have - 1) * ld + c, reduce - c);
         }
         const int r = 32 * s + (tid >> 3), c = 8 * (tid & 7);
@@ -608,12 +610,16 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
                 to.inner0 = tm * TM;
                 to.outer0 = tn * TN;
                 to.outer_end = (int)job.outer;
-                const auto end = [&](int e) __attribute__((always_inline)) {
-                    if constexpr (LONG) return lds<ExpertRows>().end[e];
-                    else return end_of(job.ends, e, job.rows);
-                };
-                const int first = uniform(to.expert == 0 ? 0 : end(to.expert - 1));
-                to.reduce = (int64_t)uniform(max(end(to.expert) - first, 0)) * T::kSize;
+                int first, end;
+                if constexpr (LONG) {
+                    const ExpertRows& table = lds<ExpertRows>();
+                    first = to.expert == 0 ? 0 : table.end[to.expert - 1];
+                    end = table.end[to.expert];
+                } else {
+                    rows_of(job.ends, job.rows, to.expert, &first, &end);
+                }
+                first = uniform(first);
+                to.reduce = (int64_t)uniform(end - first) * T::kSize;
                 a += first * job.lda + (int64_t)to.inner0 * T::kSize;
                 b += first * job.ldb + (int64_t)to.outer0 * T::kSize;
             }

@@ -11,7 +11,7 @@ namespace {
 
 using namespace tsenor;
 
-constexpr int64_t kMaxEntries = int64_t(1) << 40, kMaxRows = int64_t(1) << 31, kMaxReduce = int64_t(1) << 17;
+constexpr int64_t kMaxEntries = int64_t(1) << 40, kMaxRows = int64_t(1) << 30, kMaxReduce = int64_t(1) << 17;
 constexpr int64_t kMaxExperts = 1024;
 
 bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
@@ -125,7 +125,7 @@ int tsenor_grouped_mm(const uint16_t* X, int64_t rows, int64_t ldx, const uint16
     if (!float_type(ytype)) return TSENOR_ERR_DTYPE;
     if ((transpose != 0 && transpose != 1) || experts < 1 || experts > kMaxExperts) return TSENOR_ERR_PARAM;
     const int64_t wrows = transpose ? k : m, wcols = transpose ? m : k;
-    if (rows < 0 || rows >= kMaxRows || m <= 0 || k <= 0 || ldx < k || ldy < m || ldw < wcols || too_big(rows, ldx) ||
+    if (rows < 0 || rows >= kMaxRows || m <= 0 || k <= 0 || k >= kMaxRows || ldx < k || ldy < m || ldw < wcols || too_big(rows, ldx) ||
         too_big(rows, ldy) || too_big(wrows, ldw) || (experts > 1 && stride < wrows * ldw) || too_big(experts, stride))
         return TSENOR_ERR_SHAPE;
     if (misaligned(X, 2) || misaligned(W, 2) || misaligned(ends, 4) || misaligned(Y, element_size(ytype)))

@@ -84,7 +84,7 @@ struct RowTile {
     int first, end;  // rows first .. min(first + tile, end) - 1
 };
 
-// Sum over the lanes up to each one, and each lane's value from the lane before (0 for the first): DPP
+// Sum and maximum over the lanes up to each one, and each lane's value from the lane before (0 for the first): DPP
 // moves along rows of 16 lanes, then each row's last value into the rows behind.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int from_lane(int v) {
@@ -99,10 +99,36 @@ __device__ __forceinline__ int sum_up_to(int v) {
     v += from_lane<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
     return v;
 }
+__device__ __forceinline__ int max_up_to(int v) {  // of values that are not negative
+    v = max(v, from_lane<0x111, 0xF>(v));
+    v = max(v, from_lane<0x112, 0xF>(v));
+    v = max(v, from_lane<0x114, 0xF>(v));
+    v = max(v, from_lane<0x118, 0xF>(v));
+    v = max(v, from_lane<0x142, 0xA>(v));
+    return max(v, from_lane<0x143, 0xC>(v));
+}
 __device__ __forceinline__ int lane_before(int v) { return from_lane<0x138, 0xF>(v); }  // wave_shr 1
 
-// An entry of `ends` as it counts.
-__device__ __forceinline__ int end_of(const int* ends, int e, int rows) { return min(max(ends[e], 0), rows); }
+// Where the rows of experts e0 .. e0 + 63 end, one expert a lane: the largest entry up to its own, within
+// 0 .. rows (so that whatever `ends` holds, experts never share a row).  `before`: that of the expert
+// before e0, or 0; behind the last expert it stays.
+__device__ __forceinline__ int end_of_lane(const int* ends, int experts, int rows, int e0, int before) {
+    const int e = e0 + (threadIdx.x & 63);
+    return max(max_up_to(e < experts ? min(max(ends[e], 0), rows) : 0), before);
+}
+// Rows first .. end - 1 of one expert, the same in all lanes.
+__device__ __forceinline__ void rows_of(const int* ends, int rows, int expert, int* first, int* end) {
+    int last = 0;
+    for (int e0 = 0;; e0 += 64) {
+        const int hi = end_of_lane(ends, expert + 1, rows, e0, last);
+        if (expert < e0 + 64) {
+            *first = expert == e0 ? last : __builtin_amdgcn_readlane(hi, expert - e0 - 1);
+            *end = __builtin_amdgcn_readlane(hi, expert - e0);
+            return;
+        }
+        last = __builtin_amdgcn_readlane(hi, 63);
+    }
+}
 
 // Tiles of `size` rows, expert after expert, then those of no expert: tile t, or their number
 // in *tiles when t < 0 (64 experts at a time, one a lane).  Every lane gets the same answer.
@@ -120,10 +146,10 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
     } else {
         for (int e0 = 0; e0 < experts; e0 += 64) {
             const int e = e0 + lane;
-            const int hi = e < experts ? end_of(ends, e, rows) : 0;
+            const int hi = end_of_lane(ends, experts, rows, e0, last);
             int lo = lane_before(hi);
             if (lane == 0) lo = last;
-            const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
+            const int n = e < experts ? (hi - lo + size - 1) / size : 0;
             const int sum = sum_up_to(n);
             const uint64_t behind = __ballot(t >= 0 && before + sum > t);
             if (behind != 0) {
@@ -134,7 +160,7 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
                 return true;
             }
             before += __builtin_amdgcn_readlane(sum, 63);
-            last = __builtin_amdgcn_readlane(hi, min(63, experts - 1 - e0));
+            last = __builtin_amdgcn_readlane(hi, 63);
         }
     }
     if (tiles != nullptr) *tiles = before + (rows - last + size - 1) / size;
@@ -155,11 +181,15 @@ struct ExpertRows {
     int end[kMaxExperts], order[64];
 };
 __device__ __forceinline__ void expert_rows(const int* ends, int experts, int rows, ExpertRows& table) {
-    for (int e = threadIdx.x; e < experts; e += blockDim.x) table.end[e] = end_of(ends, e, rows);
-    if (experts > 64) return;
     const int lane = threadIdx.x & 63;
-    const int hi = lane < experts ? end_of(ends, lane, rows) : 0, lo = lane_before(hi);
-    const int n = lane < experts ? hi - (lane == 0 ? 0 : lo) : 0;
+    int last = 0, n = 0;  // rows of the first 64 experts, one a lane
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        const int hi = end_of_lane(ends, experts, rows, e0, last);
+        if (e0 + lane < experts && threadIdx.x < 64) table.end[e0 + lane] = hi;
+        if (e0 == 0) n = lane < experts ? hi - lane_before(hi) : 0;
+        last = __builtin_amdgcn_readlane(hi, 63);
+    }
+    if (experts > 64) return;
     int rank = 0;
     for (int e = 0; e < experts; ++e) {
         const int o = __builtin_amdgcn_readlane(n, e);
@@ -178,17 +208,17 @@ __device__ __forceinline__ int row_table(const int* ends, int experts, int rows,
     int before = 0, last = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
         const int e = e0 + lane;
-        const int hi = e >= experts ? 0 : ends == nullptr ? rows : end_of(ends, e, rows);
-        int lo = lane_before(hi);
+        const int hi = ends == nullptr ? rows : end_of_lane(ends, experts, rows, e0, last);
+        int lo = ends == nullptr ? 0 : lane_before(hi);
         if (lane == 0) lo = last;
-        const int n = e < experts ? (max(hi - lo, 0) + size - 1) / size : 0;
+        const int n = e < experts ? (hi - lo + size - 1) / size : 0;
         const int sum = sum_up_to(n);
         if (e < experts && threadIdx.x < 64) {
             table.tile[e] = before + sum - n;
             table.row[e] = lo;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
-        last = __builtin_amdgcn_readlane(hi, min(63, experts - 1 - e0));
+        last = __builtin_amdgcn_readlane(hi, 63);
     }
     if (threadIdx.x == 0) {
         table.tile[experts] = before;

@@ -5,9 +5,8 @@ import numpy as np
 
 def bounds(ends, rows):
     """(first, end) of every expert, entries of `ends` as they count."""
-    e = np.clip(np.asarray(ends, np.int64), 0, rows)
-    first = np.concatenate([[0], e[:-1]])
-    return list(zip(first.tolist(), np.maximum(first, e).tolist()))
+    e = np.maximum.accumulate(np.clip(np.asarray(ends, np.int64), 0, rows))
+    return list(zip([0] + e[:-1].tolist(), e.tolist()))
 
 
 def grouped_mm(x, w, ends, transpose):

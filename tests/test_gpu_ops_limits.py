@@ -97,19 +97,21 @@ def test_ends_outside_the_rows(ends):
     exactly(sms.grouped_wgrad(dy, x, e), ref.grouped_wgrad(dyv, xv, ends)[0])
 
 
-def test_descending_ends_stay_in_bounds():
-    """Which product a row gets is unspecified then; what lies around the result stays as it was."""
+@pytest.mark.parametrize("rows,m,k", [(50, 64, 64), (400, 256, 64), (3000, 2048, 64), (50, 65, 33)])
+def test_descending_ends(rows, m, k):
+    """An entry below an earlier one counts as that one; what lies around the result stays as it was."""
     import torch
     rng = np.random.default_rng(2)
-    for rows, m, k in ((50, 64, 64), (3000, 2048, 64)):
-        e = torch.tensor([rows, 3, rows // 2, 0, rows + 9, 1], dtype=torch.int32).cuda()
-        x, _ = bf16(ints(rng, (rows, k)))
-        w, _ = bf16(ints(rng, (6, m, k)))
+    few, many = [rows // 3, 3, rows // 2, 0, rows // 2 + 1, -7, rows - 2, 1], rng.integers(-5, rows, 130).tolist()
+    for ends in (few, many, [rows + 9, 0, 5]):
+        experts, e = len(ends), torch.tensor(ends, dtype=torch.int32).cuda()
+        x, xv = bf16(ints(rng, (rows, k)))
+        w, wv = bf16(ints(rng, (experts, m, k)))
+        dy, dyv = bf16(ints(rng, (rows, m)))
         buf = torch.full((rows + 2, m + 8), 7.0, device="cuda", dtype=torch.bfloat16)
-        sms.grouped_mm(x, w, e, out=buf[1:-1, :m])
+        exactly(sms.grouped_mm(x, w, e, out=buf[1:-1, :m]), ref.grouped_mm(xv, wv, ends, False)[0])
         assert (buf[0] == 7).all() and (buf[-1] == 7).all() and (buf[:, m:] == 7).all()
-        dy, _ = bf16(ints(rng, (rows, m)))
-        assert torch.isfinite(sms.grouped_wgrad(dy, x, e).float()).all()
+        exactly(sms.grouped_wgrad(dy, x, e), ref.grouped_wgrad(dyv, xv, ends)[0])
 
 
 def _views(rng, shape, offset, pad):

@@ -45,8 +45,8 @@ def mm(X=FAKE, rows=20, ldx=64, W=FAKE, tr=0, experts=4, stride=96 * 64, ldw=64,
 @pytest.mark.parametrize("kw,code", [
     (dict(X=None), NULL), (dict(W=None), NULL), (dict(ends=None), NULL), (dict(Y=None), NULL), (dict(yt=2), DTYPE),
     (dict(tr=2), PARAM), (dict(tr=-1), PARAM), (dict(experts=0), PARAM), (dict(experts=1025, stride=0), PARAM),
-    (dict(rows=-1), SHAPE), (dict(rows=1 << 31), SHAPE), (dict(m=0), SHAPE), (dict(k=0), SHAPE), (dict(ldx=63), SHAPE),
-    (dict(ldw=63), SHAPE), (dict(ldy=95), SHAPE), (dict(stride=96 * 64 - 1), SHAPE), (dict(tr=1, ldw=95), SHAPE),
+    (dict(rows=-1), SHAPE), (dict(rows=1 << 30), SHAPE), (dict(m=0), SHAPE), (dict(k=0), SHAPE), (dict(ldx=63), SHAPE),
+    (dict(k=1 << 30, ldx=1 << 30, ldw=1 << 30, stride=1 << 37, rows=1), SHAPE), (dict(ldw=63), SHAPE), (dict(ldy=95), SHAPE), (dict(stride=96 * 64 - 1), SHAPE), (dict(tr=1, ldw=95), SHAPE),
     (dict(X=ODD), SHAPE), (dict(W=ODD), SHAPE), (dict(ends=ctypes.c_void_p(0x1002)), SHAPE), (dict(Y=ODD), SHAPE),
     (dict(yt=0, Y=ctypes.c_void_p(0x1002)), SHAPE), (dict(k=1 << 41, ldx=1 << 41, ldw=1 << 41), SHAPE),
     (dict(rows=(1 << 31) - 1, ldx=1 << 30, stride=1 << 62), SHAPE), (dict(rows=0, X=None, Y=None), OK),
