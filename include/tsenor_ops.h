@@ -90,8 +90,8 @@ int tsenor_quant_int8(const void* X, int dtype, int64_t batch, int64_t stride, i
  *   ends   as above, or NULL: one weight (experts 1) for all rows;
  *   Y      ytype f32 or bf16, [rows][ldy], ldy >= m.
  * rows == 0 is a no-op.  Errors: _NULL, _DTYPE, _PARAM (experts < 1 or > 1024,
- * experts != 1 without ends), _SHAPE (rows < 0 or >= 2^30, m, k <= 0, k > 2^17,
- * leading dimensions, more rows than allowed for bf16, alignment: values 16 bytes). */
+ * experts != 1 without ends), _SHAPE (rows < 0 or >= 2^30, m <= 0 or >= 2^30,
+ * k <= 0 or > 2^17, leading dimensions, more rows than allowed for bf16, alignment: values 16 bytes). */
 int tsenor_gemm_int8(const void* X, int xtype, const float* xscales, int64_t rows, int64_t ldx,
                      const int8_t* A, const float* ascales, int64_t experts, int64_t m, int64_t k,
                      const int* ends, void* Y, int ytype, int64_t ldy, void* stream);

@@ -44,7 +44,7 @@ def _bf16_matrix(torch, t, name, device=None, dim=2):
 
 def _stack_strides(t):
     """From matrix to matrix of a stack, from row to row (a single one may have any stride)."""
-    ld = _ld(t)
+    ld = t.shape[-1] if t.shape[-2] == 1 else t.stride(-2)
     return (t.shape[-2] * ld if t.shape[0] == 1 else t.stride(0)), ld
 
 
@@ -78,7 +78,7 @@ def _result(torch, out, shape, dtype, near, inputs):
                          + (f" and type {dtype}" if dtype is not None else ""))
     if shape[-2] > 1 and out.stride(-2) < shape[-1]:
         raise ValueError("the rows of out overlap")
-    if len(shape) == 3 and shape[0] > 1 and out.stride(0) < shape[1] * _ld(out):
+    if len(shape) == 3 and shape[0] > 1 and out.stride(0) < shape[1] * _stack_strides(out)[1]:
         raise ValueError("the matrices of out overlap")
     _separate(out, inputs)
     return out

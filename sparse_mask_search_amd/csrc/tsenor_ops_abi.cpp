@@ -125,8 +125,10 @@ int tsenor_grouped_mm(const uint16_t* X, int64_t rows, int64_t ldx, const uint16
     if (!float_type(ytype)) return TSENOR_ERR_DTYPE;
     if ((transpose != 0 && transpose != 1) || experts < 1 || experts > kMaxExperts) return TSENOR_ERR_PARAM;
     const int64_t wrows = transpose ? k : m, wcols = transpose ? m : k;
-    if (rows < 0 || rows >= kMaxRows || m <= 0 || k <= 0 || k >= kMaxRows || ldx < k || ldy < m || ldw < wcols || too_big(rows, ldx) ||
-        too_big(rows, ldy) || too_big(wrows, ldw) || (experts > 1 && stride < wrows * ldw) || too_big(experts, stride))
+    if (rows < 0 || rows >= kMaxRows || m <= 0 || k <= 0 || k >= kMaxRows || ldx < k || ldy < m || ldw < wcols)
+        return TSENOR_ERR_SHAPE;
+    if (too_big(rows, ldx) || too_big(rows, ldy) || too_big(wrows, ldw) || (experts > 1 && stride < wrows * ldw) ||
+        too_big(experts, stride))
         return TSENOR_ERR_SHAPE;
     if (misaligned(X, 2) || misaligned(W, 2) || misaligned(ends, 4) || misaligned(Y, element_size(ytype)))
         return TSENOR_ERR_SHAPE;
@@ -205,10 +207,12 @@ int tsenor_gemm_int8(const void* X, int xtype, const float* xscales, int64_t row
         return TSENOR_ERR_NULL;
     if ((!ready && xtype != TSENOR_BF16) || !float_type(ytype)) return TSENOR_ERR_DTYPE;
     if (experts < 1 || experts > kMaxExperts || (ends == nullptr && experts != 1)) return TSENOR_ERR_PARAM;
-    if (rows < 0 || rows >= kMaxRows || m <= 0 || k <= 0 || k > kMaxReduce || ldy < m) return TSENOR_ERR_SHAPE;
+    if (rows < 0 || rows >= kMaxRows || m <= 0 || m >= kMaxRows || k <= 0 || k > kMaxReduce || ldy < m)
+        return TSENOR_ERR_SHAPE;
     const int64_t kpad = (k + 127) / 128 * 128;
-    if ((ready ? ldx != kpad : ldx < k || rows > 16 || rows * kpad > kMaxTokenEntries || ends != nullptr) || too_big(rows, ldx) || too_big(rows, ldy) ||
-        too_big(m, kpad) || too_big(experts, m * kpad))
+    if (ready ? ldx != kpad : ldx < k || rows > 16 || rows * kpad > kMaxTokenEntries || ends != nullptr)
+        return TSENOR_ERR_SHAPE;
+    if (too_big(rows, ldx) || too_big(rows, ldy) || too_big(m, kpad) || too_big(experts, m * kpad))
         return TSENOR_ERR_SHAPE;
     if (misaligned(X, ready ? 16 : 2) || misaligned(xscales, 4) || misaligned(A, 16) || misaligned(ascales, 4) ||
         misaligned(ends, 4) || misaligned(Y, element_size(ytype)))

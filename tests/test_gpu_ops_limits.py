@@ -206,6 +206,26 @@ def test_quant_int8_stacks_and_views(dtype):
     assert sms.quant_int8(big[:0]).values.shape == (0, 9, 384) and sms.quant_int8(big[0, :0]).scales.shape == (0,)
 
 
+def test_stacks_of_single_rows():
+    """A matrix of one row may have any row stride: here more than that from matrix to matrix."""
+    import torch
+    rng = np.random.default_rng(6)
+    counts = [3, 0, 5]
+    e = ends_of(counts)
+    x, xv = bf16(ints(rng, (8, 40)))
+    y, yv = bf16(ints(rng, (8, 1)))
+    w, wv = bf16(ints(rng, (7, 3, 40)))
+    w, wv = w.transpose(0, 1)[:, 2:3], wv.transpose(1, 0, 2)[:, 2:3]
+    assert w.stride(1) > w.stride(0)
+    exactly(sms.grouped_mm(x, w, e), ref.grouped_mm(xv, wv, np.cumsum(counts), False)[0])
+    exactly(sms.grouped_mm(y, w, e, transpose=True), ref.grouped_mm(yv, wv, np.cumsum(counts), True)[0])
+    out = torch.full((7, 3, 40), 5.0, device="cuda", dtype=torch.float32)
+    exactly(sms.grouped_wgrad(y, x, e, out=out.transpose(0, 1)[:, 2:3]), ref.grouped_wgrad(yv, xv, np.cumsum(counts))[0])
+    assert (out[:2] == 5).all() and (out[3:] == 5).all()
+    q, (values, scales) = sms.quant_int8(w), ref.quant_int8(wv.astype(np.float32))
+    assert np.array_equal(q.values.cpu().numpy(), values) and np.array_equal(q.scales.cpu().numpy(), scales)
+
+
 def test_longest_integer_rows():
     """k = 2^17 of 127 * 127: 2^17 * 127^2 = 2114060288 < 2^31."""
     import torch

@@ -46,7 +46,8 @@ def mm(X=FAKE, rows=20, ldx=64, W=FAKE, tr=0, experts=4, stride=96 * 64, ldw=64,
     (dict(X=None), NULL), (dict(W=None), NULL), (dict(ends=None), NULL), (dict(Y=None), NULL), (dict(yt=2), DTYPE),
     (dict(tr=2), PARAM), (dict(tr=-1), PARAM), (dict(experts=0), PARAM), (dict(experts=1025, stride=0), PARAM),
     (dict(rows=-1), SHAPE), (dict(rows=1 << 30), SHAPE), (dict(m=0), SHAPE), (dict(k=0), SHAPE), (dict(ldx=63), SHAPE),
-    (dict(k=1 << 30, ldx=1 << 30, ldw=1 << 30, stride=1 << 37, rows=1), SHAPE), (dict(ldw=63), SHAPE), (dict(ldy=95), SHAPE), (dict(stride=96 * 64 - 1), SHAPE), (dict(tr=1, ldw=95), SHAPE),
+    (dict(k=1 << 30, ldx=1 << 30, ldw=1 << 30, stride=1 << 37, rows=1), SHAPE), (dict(ldw=63), SHAPE),
+    (dict(ldy=95), SHAPE), (dict(stride=96 * 64 - 1), SHAPE), (dict(tr=1, ldw=95), SHAPE),
     (dict(X=ODD), SHAPE), (dict(W=ODD), SHAPE), (dict(ends=ctypes.c_void_p(0x1002)), SHAPE), (dict(Y=ODD), SHAPE),
     (dict(yt=0, Y=ctypes.c_void_p(0x1002)), SHAPE), (dict(k=1 << 41, ldx=1 << 41, ldw=1 << 41), SHAPE),
     (dict(rows=(1 << 31) - 1, ldx=1 << 30, stride=1 << 62), SHAPE), (dict(rows=0, X=None, Y=None), OK),
@@ -103,6 +104,7 @@ def gemm(X=FAKE, xt=3, xs=FAKE, rows=20, ldx=128, A=FAKE, as_=FAKE, experts=4, m
     (dict(xt=1, xs=None, ldx=100, experts=1, ends=None, rows=17), SHAPE),      # at most 16
     (dict(xt=1, xs=None, ldx=99, experts=1, ends=None, rows=16), SHAPE),
     (dict(xt=1, xs=None, ldx=100, experts=1, ends=None, X=ODD, rows=16), SHAPE),
+    (dict(m=1 << 30, ldy=1 << 30, experts=1), SHAPE), (dict(rows=1 << 30), SHAPE),
     (dict(rows=0, X=None, Y=None, xs=None), OK),
 ])
 def test_gemm_int8_rejects(kw, code):
