@@ -876,28 +876,37 @@ int tile(const GroupedJob& job, void* stream) {
 // workgroup on a CU, 28 with two (weight gradients: 27 and, with four, 50).  Examples (us), in that order: 1542 rows
 // 2048 x 5952 102 / 77 / 55 / 94; 600 rows 8192 x 4096 76 / 56 / 70 / 84; 600 rows of 16 experts 2048 x 4096
 // 95 / 89 / 67 / 77; 2048 rows of them 111 / 94 / 102 / 130; 4096 rows 116 / 153 / 146 / 203; data gradients, 200 rows of
-// 8 experts 2048 x 4096 62 / 55 / 40 / 27; 16384 rows of 8 experts 11008 x 4096 1252 / 1645 / 2047 / 3972; weight
-// gradients, 8192 rows 2048 x 2048 164 / - / 86 / 127, 1001 rows of 4 experts 1024 x 1024 21 / - / 12 / 10.
+// 8 experts 2048 x 4096 62 / 55 / 40 / 27; 16384 rows of 8 experts 11008 x 4096 1252 / 1645 / 2047 / 3972.
+// A weight gradient's reduction is short, so that beginning and ending a tile counts too: 7, 6 and 4 us a round, and
+// 4 and 2.5 us once with a ring of more than 64 KB; where each workgroup has one tile, the largest expert's
+// rows count (taken as 1.6 times the mean), else a third of what they exceed it by.  Examples, 256 x 256 / 128 x
+// 128 / 64 x 64: 8192 rows 2048 x 2048 164 / 86 / 127; experts 1024 x 1024, 1024 rows of 4: 18 / 12 / 10, 4096 rows of
+// 8: 29 / 24 / 21, 8000 rows: 46 / 37 / 37, 8192 rows of 16: 35 / 45 / 44; 2048 rows of 16 experts 2048 x 2048 46 / 96 / 85.
 enum Tile { k256x256, k256x128, k128x128, k64x64 };
 template <Kind K>
 Tile pick_tile(const GroupedJob& job) {
     const auto rounds = [&](int64_t m, int64_t n, int64_t at_once) {
         return (tiles_of<K>(job, m, n) + at_once - 1) / at_once;
     };
+    const double steps = K == kGradient ? job.rows / (32. * job.experts) : 1.;
+    const auto cost = [&](int64_t count, double step, double begin, double once) {
+        if (K == kProduct) return count * step;
+        return count * (step * steps * (job.experts == 1 ? 1. : count == 1 ? 1.6 : 1.2) + begin) + once;
+    };
     Tile best = k256x256;
-    int64_t least = 60 * rounds(256, 256, kCus);
-    const auto take = [&](Tile tile, int64_t cost) {
+    double least = cost(rounds(256, 256, kCus), 60, 700, 400);
+    const auto take = [&](Tile tile, double cost) {
         if (cost < least) {
             best = tile;
             least = cost;
         }
     };
-    if (K == kProduct) take(k256x128, 43 * rounds(256, 128, kCus));
-    take(k128x128, 31 * rounds(128, 128, kCus));
+    if (K == kProduct) take(k256x128, cost(rounds(256, 128, kCus), 43, 0, 0));
+    take(k128x128, cost(rounds(128, 128, kCus), 31, 600, 250));
     const int64_t small = tiles_of<K>(job, 64, 64);
-    if (small <= kCus) take(k64x64, K == kProduct ? 19 : 27);
-    else if (K == kGradient) take(k64x64, 50 * rounds(64, 64, 4 * kCus));
-    else take(k64x64, std::max<int64_t>(28, 28 * small / (2 * kCus)));  // these do not go in rounds
+    if (K == kProduct) take(k64x64, small <= kCus ? 19. : std::max(28., 28. * small / (2 * kCus)));  // not in rounds
+    else if (small <= kCus) take(k64x64, 27 * steps + 400);
+    else take(k64x64, rounds(64, 64, 4 * kCus) * (50 * steps + 400));  // a CU's four have different experts' rows
     return best;
 }
 

@@ -55,6 +55,21 @@ def test_grouped_wgrad_forms(rows, experts, m, k, masked):
     exactly(sms.grouped_wgrad(dy, x, ends_of(counts), mask=words(keep) if masked else None), want)
 
 
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,experts,m,k", [(2600, 1, 1792, 2056), (6000, 2, 1280, 1808), (1700, 5, 520, 1544)])
+def test_grouped_wgrad_middle_tiles(rows, experts, m, k, dtype, masked):
+    """128 x 128 with one tile and with more for a workgroup; 64 x 64 with more than one for a CU."""
+    say("middle tiles", rows, experts, m, k, dtype, masked)
+    rng = np.random.default_rng(rows + k)
+    counts = spread(rng, rows - 5, experts)
+    x, xv = bf16(ints(rng, (rows, k)))
+    dy, dyv = bf16(ints(rng, (rows, m)))
+    keep = rng.random((experts, m, k)) < 0.5 if masked else None
+    want, _ = ref.grouped_wgrad(dyv, xv, np.cumsum(counts), keep)
+    exactly(sms.grouped_wgrad(dy, x, ends_of(counts), mask=words(keep) if masked else None, dtype=torch_type(dtype)), want)
+
+
 @pytest.mark.parametrize("rows,experts,m,k", [(2500, 6, 4096, 500), (9000, 3, 2304, 700), (300, 8, 512, 200)])
 def test_gemm_int8_forms(rows, experts, m, k):
     import torch
