@@ -11,7 +11,9 @@ namespace {
 
 using namespace ops;
 
-// G threads hold a row of up to 64 G entries (8 V at 8 a vector) in registers, read once.
+// G threads hold a row of up to 8 V G entries in registers (V vectors of 8 each), so that it is read once; a
+// wave's shuffles, or four waves' LDS words, give its largest magnitude.  Memory bounds it: bf16 11008 x 4096 in
+// 26 to 29 us (4.7 to 5.2 TB/s).
 template <class T, int G, int V>
 __global__ __launch_bounds__(256) void quant_int8_kernel(const T* __restrict__ X, int64_t stride, int64_t rows,
                                                          int64_t all, int64_t cols, int64_t ldx, bool vec,
