@@ -70,7 +70,7 @@ __device__ __forceinline__ void finish(const GroupedJob& job, int expert, int64_
 // Any alignment and any size: tiles of 64 x 64, four waves of 32 x 32, operands through
 // registers into two LDS buffers.  AT, BT: the operand is contiguous along its columns.  Loads that straddle
 // lines bound it: 8192 rows of 16 experts 4095 x 2047, data gradients 764 us (180 TFLOP/s; 16-byte aligned rows,
-// by the tiles below, 167).
+// by the tiles below, 161).
 template <class T, bool AT, bool BT, Kind K, class TO>
 __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) {
     __shared__ u32x4 ta[2][256], tb[2][256];
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
 // Measured: 8192 x 8192 x 8192 807 us, 1.36 PFLOP/s, the matrix cores 74% busy at 1.50 GHz: the card's power bounds it
 // (the plain library product 758 us).  16384 rows of 8 experts 11008 x 4096 1.26 ms (1.17 PFLOP/s), 8192 of 8-bit
 // integers 358 us (2.06 POP/s): the last round of tiles too.  8192 rows of 16 experts 2048 x 4096: data gradients
-// 167 us (44% busy at 2.1 GHz; 127 with as many rows for each), weight gradients under masks 161 us, of which 42 us are
+// 161 us (44% busy at 2.1 GHz; 127 with as many rows for each), weight gradients under masks 161 us, of which 42 us are
 // the results' way out: a step's wait is for the stores before it too.
 
 constexpr int64_t kCus = 256;
@@ -544,6 +544,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
     typedef Loads<T, AT, TM, W> LoadsA;
     typedef Loads<T, BT, TN, W> LoadsB;
     constexpr bool kMasked = K == kGradient && LONG;
+    constexpr int kHalf = TB > 1 ? TN / 2 : 0;  // an expert's last rows, if they are no more, take half a tile's products
     static_assert(DIRECT ? R >= 4 : R == 3 && !AT && !BT, "ring");
     struct Buffer {
         u32x4 a[TM * 4];
@@ -571,15 +572,18 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         LoadsB lb;
     };
     int total, work = blockIdx.x;  // work of the launch (it fits a grid); this workgroup's next piece
-    int tiles = 0;                                // row tiles
-    if constexpr (K == kProduct && LONG) {
-        tiles = row_table(job.ends, job.experts, job.rows, TN, lds<RowTable>());
+    if constexpr (K == kProduct) {
+        static_assert(LONG, "products");
+        const RowTable& table = lds<RowTable>();
+        // Half tiles go behind all others where workgroups have few tiles, so that none begins a whole one last: 8192
+        // rows of 16 experts 2048 x 4096 204 -> 189 us, 4096 x 2048 transposed 166 -> 161, 4096 rows of 8 11008 x 4096 416 ->
+        // 426.  With more they are farther from those that read the same weights, for nothing: 16384 rows of 8
+        // experts 11008 x 4096 1253 -> 1266 us.
+        const bool last = across * (int64_t)(job.rows / TN) < 4 * (int64_t)gridDim.x;
+        row_table(job.ends, job.experts, job.rows, TN, last ? kHalf : 0, lds<RowTable>());
         __syncthreads();
-        total = across * uniform(tiles);
-    } else if constexpr (K == kProduct) {
-        RowTile none;
-        row_tile(job.ends, job.experts, job.rows, TN, -1, &none, &tiles);
-        total = across * uniform(tiles);
+        const int none = job.rows - uniform(table.row[job.experts]);
+        total = across * (uniform(table.tile[job.experts] + table.tail[job.experts]) + (none + TN - 1) / TN);
     } else {
         total = across * down * job.experts;
         if constexpr (LONG) {
@@ -593,14 +597,27 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             const uint8_t *a = static_cast<const uint8_t*>(job.a), *b = static_cast<const uint8_t*>(job.b);
             int tm = 0, tn = 0;
             if constexpr (K == kProduct) {
-                RowTile t;
-                grid_tile(in_order(work, total), across, uniform(tiles), tm, tn);
-                if constexpr (LONG) t = row_tile_of(lds<RowTable>(), job.experts, job.rows, TN, tn);
-                else row_tile(job.ends, job.experts, job.rows, TN, tn, &t);
-                to.expert = uniform(t.expert);
+                // tiles, half tiles, rows of no expert
+                const RowTable& table = lds<RowTable>();
+                const int tiles = uniform(table.tile[job.experts]), w = work - across * tiles;
+                if (w < 0) {
+                    grid_tile(in_order(work, across * tiles), across, tiles, tm, tn);
+                    to.expert = uniform(expert_of(table.tile, job.experts, tn));
+                    to.outer0 = uniform(table.row[to.expert]) + (tn - uniform(table.tile[to.expert])) * TN;
+                    to.outer_end = uniform(table.row[to.expert + 1]);
+                } else if (const int tails = uniform(table.tail[job.experts]); w < across * tails) {
+                    grid_tile(in_order(w, across * tails), across, tails, tm, tn);
+                    to.expert = uniform(expert_of(table.tail, job.experts, tn));
+                    to.outer_end = uniform(table.row[to.expert + 1]);
+                    to.outer0 = to.outer_end - (to.outer_end - uniform(table.row[to.expert])) % TN;
+                } else {
+                    tn = (w - across * tails) / across;
+                    tm = w - across * (tails + tn);
+                    to.expert = -1;
+                    to.outer0 = uniform(table.row[job.experts]) + tn * TN;
+                    to.outer_end = job.rows;
+                }
                 to.inner0 = tm * TM;
-                to.outer0 = uniform(t.first);
-                to.outer_end = uniform(t.end);
                 to.reduce = to.expert < 0 ? 0 : job.kbytes;
                 a += to.expert * job.astride + (AT ? (int64_t)to.inner0 * T::kSize : to.inner0 * job.lda);
                 b += to.outer0 * job.ldb;
@@ -812,8 +829,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
             for (; t + (DIRECT ? R : 4) < cur.full; t += 2) two_steps(Inside(), pairs);
             for (; t < cur.steps; t += 2) two_steps(AtEnd(), pairs);
         };
-        // an expert's last rows fill half a tile at most as often as not
-        if (K == kProduct && TB > 1 && cur.outer_end - cur.outer0 <= TN / 2) all_steps(Count<TB / 2 + (TB == 1)>());
+        if (K == kProduct && cur.outer_end - cur.outer0 <= kHalf) all_steps(Count<TB / 2 + (TB == 1)>());
         else all_steps(Count<TB>());
         const int row0 = cur.outer0 + 16 * wn + (lane & 15), c0 = cur.inner0 + (TM / WM) * wm;
         const uint32_t* kept =

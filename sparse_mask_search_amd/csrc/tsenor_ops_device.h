@@ -130,16 +130,15 @@ __device__ __forceinline__ void rows_of(const int* ends, int rows, int expert, i
     }
 }
 
-// Tiles of `size` rows, expert after expert, then those of no expert: tile t, or their number
-// in *tiles when t < 0 (64 experts at a time, one a lane).  Every lane gets the same answer.
-__device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows, int size, int t, RowTile* to,
-                                         int* tiles = nullptr) {
+// Tiles of `size` rows, expert after expert, then those of no expert: tile t, if there is one (64 experts at a
+// time, one a lane).  Every lane gets the same answer.
+__device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows, int size, int t, RowTile* to) {
     const int lane = threadIdx.x & 63;
     int before = 0, last = 0;
     if (ends == nullptr) {
         before = (rows + size - 1) / size;
         last = rows;
-        if (t >= 0 && t < before) {
+        if (t < before) {
             *to = {0, t * size, rows};
             return true;
         }
@@ -151,7 +150,7 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
             if (lane == 0) lo = last;
             const int n = e < experts ? (hi - lo + size - 1) / size : 0;
             const int sum = sum_up_to(n);
-            const uint64_t behind = __ballot(t >= 0 && before + sum > t);
+            const uint64_t behind = __ballot(before + sum > t);
             if (behind != 0) {
                 const int l = __builtin_ctzll(behind);
                 const int start = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(n, l);
@@ -163,8 +162,6 @@ __device__ __forceinline__ bool row_tile(const int* ends, int experts, int rows,
             last = __builtin_amdgcn_readlane(hi, 63);
         }
     }
-    if (tiles != nullptr) *tiles = before + (rows - last + size - 1) / size;
-    if (t < 0) return false;
     *to = {-1, last + (t - before) * size, rows};
     return to->first < rows;
 }
@@ -198,43 +195,48 @@ __device__ __forceinline__ void expert_rows(const int* ends, int experts, int ro
     if (threadIdx.x < experts) table.order[rank] = lane;
 }
 
-// The same from a table in LDS, which the workgroup fills once: for each expert its first tile and
-// its first row, then those of the rows that belong to none.  Returns the number of tiles.
+// The rows of all experts in LDS, which the workgroup fills once: for each expert its first row and how many
+// tiles the experts before it have, of more than `half` rows and of at most that many (an expert's last one);
+// in the last entries the first row of no expert and all tiles.
 struct RowTable {
-    int tile[kMaxExperts + 1], row[kMaxExperts + 1];
+    int row[kMaxExperts + 1], tile[kMaxExperts + 1], tail[kMaxExperts + 1];
 };
-__device__ __forceinline__ int row_table(const int* ends, int experts, int rows, int size, RowTable& table) {
+__device__ __forceinline__ void row_table(const int* ends, int experts, int rows, int size, int half, RowTable& table) {
     const int lane = threadIdx.x & 63;
-    int before = 0, last = 0;
+    int tiles = 0, tails = 0, last = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
         const int e = e0 + lane;
         const int hi = ends == nullptr ? rows : end_of_lane(ends, experts, rows, e0, last);
         int lo = ends == nullptr ? 0 : lane_before(hi);
         if (lane == 0) lo = last;
-        const int n = e < experts ? (hi - lo + size - 1) / size : 0;
-        const int sum = sum_up_to(n);
+        const int n = e < experts ? hi - lo : 0, rest = n % size;
+        const int full = n / size + (rest > half ? 1 : 0), tail = rest != 0 && rest <= half ? 1 : 0;
+        const int sum = sum_up_to(full), tail_sum = sum_up_to(tail);
         if (e < experts && threadIdx.x < 64) {
-            table.tile[e] = before + sum - n;
             table.row[e] = lo;
+            table.tile[e] = tiles + sum - full;
+            table.tail[e] = tails + tail_sum - tail;
         }
-        before += __builtin_amdgcn_readlane(sum, 63);
+        tiles += __builtin_amdgcn_readlane(sum, 63);
+        tails += __builtin_amdgcn_readlane(tail_sum, 63);
         last = __builtin_amdgcn_readlane(hi, 63);
     }
     if (threadIdx.x == 0) {
-        table.tile[experts] = before;
         table.row[experts] = last;
+        table.tile[experts] = tiles;
+        table.tail[experts] = tails;
     }
-    return before + (rows - last + size - 1) / size;
 }
-__device__ __forceinline__ RowTile row_tile_of(const RowTable& table, int experts, int rows, int size, int t) {
+// Tile t of `before` (table.tile or table.tail): the last expert before which there are no more than t.
+__device__ __forceinline__ int expert_of(const int* before, int experts, int t) {
     const int lane = threadIdx.x & 63;
-    int e = -1;  // the last expert whose first tile is not behind t: those before it with the same one have no rows
-    for (int e0 = 0; e0 <= experts; e0 += 64) {
-        const uint64_t begun = __ballot(e0 + lane <= experts && table.tile[min(e0 + lane, experts)] <= t);
+    int e = -1;
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        const uint64_t begun = __ballot(e0 + lane < experts && before[min(e0 + lane, experts)] <= t);
         e += __builtin_popcountll(begun);
         if (begun != ~uint64_t(0)) break;
     }
-    return {e == experts ? -1 : e, table.row[e] + (t - table.tile[e]) * size, e == experts ? rows : table.row[e + 1]};
+    return e;
 }
 
 // The most tiles that row_tile can give.
