@@ -27,7 +27,7 @@ struct GroupedJob {
     bool ovec, ovec8;   // four (eight bf16) neighbouring outputs may be written at once
 };
 
-// e: types of the operands; transposed: weights [k][m].  They return a hipError_t
+// transposed: weights [k][m].  They return a hipError_t
 // value or kGridTooLarge.
 int launch_grouped_mm(const GroupedJob& job, bool transposed, bool bf16out, void* stream);
 int launch_grouped_wgrad(const GroupedJob& job, bool bf16out, void* stream);
