@@ -320,8 +320,6 @@ def _grad_list(torch, grads, masks, out, write):
 
 
 def _clip(torch, grads, masks, out, max_norm):
-    if not grads:
-        raise ValueError("grads holds no tensor")
     write = max_norm is not None
     device, words = _grad_list(torch, grads, masks, out, write)
     n = len(grads)
