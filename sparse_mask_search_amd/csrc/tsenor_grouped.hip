@@ -7,8 +7,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
-
+#include "tsenor_grouped_forms.h"
 #include "tsenor_internal.h"
 #include "tsenor_ops_device.h"
 
@@ -16,8 +15,6 @@ namespace tsenor {
 namespace {
 
 using namespace ops;
-
-enum Kind { kProduct, kGradient };
 
 // Sixteen bytes at any alignment of the entries.  (Global loads by name: a pointer that the compiler
 // cannot place makes it a flat load, which waits for LDS too.)
@@ -334,9 +331,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
 // integers 358 us (2.06 POP/s): the last round of tiles too.  8192 rows of 16 experts 2048 x 4096: data gradients
 // 161 us (44% busy at 2.1 GHz; 127 with as many rows for each), weight gradients under masks 161 us, of which 42 us are
 // the results' way out: a step's wait is for the stores before it too.
-
-constexpr int64_t kCus = 256;
-constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside a tile fit 32 bits
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
@@ -870,19 +864,6 @@ int few(const GroupedJob& job, void* stream) {
     return (int)hipGetLastError();
 }
 
-// Direct loads take 16 bytes of an aligned row at a time.
-bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0;
-}
-
-// Tiles of a launch, as far as the host can know: a little more than half a tile counted for each expert.
-template <Kind K>
-int64_t tiles_of(const GroupedJob& job, int64_t m, int64_t n) {
-    const int64_t across = (job.inner + m - 1) / m;
-    return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
-                                    : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts * 9 / 16 : 0));
-}
-
 template <class T, bool AT, bool BT, Kind K, int TM, int TN, int WM, int WN, int R, bool LONG, bool DIRECT, class TO>
 int tile(const GroupedJob& job, void* stream) {
     const int64_t across = (job.inner + TM - 1) / TM;
@@ -896,83 +877,24 @@ int tile(const GroupedJob& job, void* stream) {
     return (int)hipGetLastError();
 }
 
-// The tile whose rounds of workgroups take the least time.  Measured, hundredths of a microsecond for a step
-// (64 bytes of the reduction) of one round: 256 x 256: 60; 256 x 128: 43; 128 x 128: 31; 64 x 64: 19 with one
-// workgroup on a CU, 28 with two (weight gradients: 27 and, with four, 50).  Examples (us), in that order: 1542 rows
-// 2048 x 5952 102 / 77 / 55 / 94; 600 rows 8192 x 4096 76 / 56 / 70 / 84; 600 rows of 16 experts 2048 x 4096
-// 95 / 89 / 67 / 77; 2048 rows of them 111 / 94 / 102 / 130; 4096 rows 116 / 153 / 146 / 203; data gradients, 200 rows of
-// 8 experts 2048 x 4096 62 / 55 / 40 / 27; 16384 rows of 8 experts 11008 x 4096 1252 / 1645 / 2047 / 3972.
-// A weight gradient's reduction is short, so that beginning and ending a tile counts too: 7, 6 and 4 us a round, and
-// 4 and 2.5 us once with a ring of more than 64 KB; where each workgroup has one tile, the largest expert's
-// rows count (taken as 1.6 times the mean), else a third of what they exceed it by.  Examples, 256 x 256 / 128 x
-// 128 / 64 x 64: 8192 rows 2048 x 2048 164 / 86 / 127; experts 1024 x 1024, 1024 rows of 4: 18 / 12 / 10, 4096 rows of
-// 8: 29 / 24 / 21, 8000 rows: 46 / 37 / 37, 8192 rows of 16: 35 / 45 / 44; 2048 rows of 16 experts 2048 x 2048 46 / 96 / 85.
-enum Tile { k256x256, k256x128, k128x128, k64x64 };
-template <Kind K>
-Tile pick_tile(const GroupedJob& job) {
-    const auto rounds = [&](int64_t m, int64_t n, int64_t at_once) {
-        return (tiles_of<K>(job, m, n) + at_once - 1) / at_once;
-    };
-    const double steps = K == kGradient ? job.rows / (32. * job.experts) : 1.;
-    const auto cost = [&](int64_t count, double step, double begin, double once) {
-        if (K == kProduct) return count * step;
-        return count * (step * steps * (job.experts == 1 ? 1. : count == 1 ? 1.6 : 1.2) + begin) + once;
-    };
-    Tile best = k256x256;
-    double least = cost(rounds(256, 256, kCus), 60, 700, 400);
-    const auto take = [&](Tile tile, double cost) {
-        if (cost < least) {
-            best = tile;
-            least = cost;
-        }
-    };
-    if (K == kProduct) take(k256x128, cost(rounds(256, 128, kCus), 43, 0, 0));
-    take(k128x128, cost(rounds(128, 128, kCus), 31, 600, 250));
-    const int64_t small = tiles_of<K>(job, 64, 64);
-    if (K == kProduct) take(k64x64, small <= kCus ? 19. : std::max(28., 28. * small / (2 * kCus)));  // not in rounds
-    else if (small <= kCus) take(k64x64, 27 * steps + 400);
-    else take(k64x64, rounds(64, 64, 4 * kCus) * (50 * steps + 400));  // a CU's four have different experts' rows
-    return best;
-}
-
 template <class T, bool AT, bool BT, Kind K, class TO>
 int product(const GroupedJob& job, void* stream) {
+    const Form form = pick_form<K, AT, BT>(job, T::kSize);
     if constexpr (K == kProduct && !AT) {
-        // Few rows: on average up to eight an expert, or up to 64 where tiles would leave CUs without work.
-        // Measured (us), 16 columns a wave / 64 x 64 tiles: 6 rows of 64 experts 1408 x 2048: 11 / 28; 64 rows:
-        // 47 / 47; 64 rows of 16 experts 2048 x 4096: 49 / 56; 16 rows 11008 x 4096: 21 / 24; 64 rows 4096 x
-        // 4096 18 / 25, 11008 x 4096 46 / 25.  As many columns as leave 160 workgroups: one row 4096 x 4096 in
-        // 11 / 13 / 19 for 16 / 32 / 64; 16 rows 11008 x 4096 in 26 / 28 / 21.
-        const int64_t parts = job.ends != nullptr ? std::min<int64_t>(job.rows, job.experts) : 1;
-        if (job.rows <= 16 || job.rows <= 8 * (int64_t)job.experts) {
-            if ((job.inner + 63) / 64 * parts >= 160) return few<T, false, 1, 4, TO>(job, stream);
-            if ((job.inner + 31) / 32 * parts >= 160) return few<T, false, 1, 2, TO>(job, stream);
-            return few<T, false, 1, 1, TO>(job, stream);
-        }
-        if (job.rows <= 64 && tiles_of<K>(job, 64, 64) < 128) return few<T, false, 2, 2, TO>(job, stream);
+        if (form == kFew64) return few<T, false, 1, 4, TO>(job, stream);
+        if (form == kFew32) return few<T, false, 1, 2, TO>(job, stream);
+        if (form == kFew16) return few<T, false, 1, 1, TO>(job, stream);
+        if (form == kFew32x32) return few<T, false, 2, 2, TO>(job, stream);
     }
-    if constexpr (T::kSize == 2) {  // 8-bit integers are aligned, and their rows short
-        // tiles count rows, columns and the bytes between rows in 32 bits
-        if (job.inner > (K == kGradient ? 1 << 26 : 0x7FFFFF00) || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow ||
-            job.ldb >= kMaxRow)
-            return any<T, AT, BT, K, TO>(job, stream);
-        const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
-        if (!direct(job.a, job.lda, as, AT ? job.inner * T::kSize : job.kbytes) ||
-            !direct(job.b, job.ldb, 0, BT ? job.outer * T::kSize : job.kbytes)) {
-            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5850 / 3200; 1003 rows of 16
-            // experts 2047 x 4095: 132 / 157; column-contiguous operands, 8192 rows of 16 experts 4095 x 2047: 764 / 829,
-            // weight gradients 739 / 800.
-            if constexpr (!AT && !BT)
-                if (tiles_of<K>(job, 256, 128) >= 160)
-                    return tile<T, AT, BT, K, 256, 128, 2, 4, 3, true, false, TO>(job, stream);
-            return any<T, AT, BT, K, TO>(job, stream);
-        }
+    if constexpr (T::kSize == 2) {
+        if constexpr (!AT && !BT)
+            if (form == kStaged256x128) return tile<T, AT, BT, K, 256, 128, 2, 4, 3, true, false, TO>(job, stream);
+        if (form == kAny) return any<T, AT, BT, K, TO>(job, stream);
     }
-    const Tile variant = pick_tile<K>(job);
-    if (variant == k256x256) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, true, TO>(job, stream);
-    if (variant == k128x128) return tile<T, AT, BT, K, 128, 128, 2, 4, 8, true, true, TO>(job, stream);
+    if (form == k256x256) return tile<T, AT, BT, K, 256, 256, 2, 4, 4, true, true, TO>(job, stream);
+    if (form == k128x128) return tile<T, AT, BT, K, 128, 128, 2, 4, 8, true, true, TO>(job, stream);
     if constexpr (K == kProduct) {
-        if (variant == k256x128) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, true, TO>(job, stream);
+        if (form == k256x128) return tile<T, AT, BT, K, 256, 128, 2, 4, 6, true, true, TO>(job, stream);
         return tile<T, AT, BT, K, 64, 64, 2, 2, 8, true, true, TO>(job, stream);
     } else {
         return tile<T, AT, BT, K, 64, 64, 2, 2, 4, false, true, TO>(job, stream);

@@ -1,0 +1,106 @@
+// tsenor_grouped_forms.h -- which kernel of tsenor_grouped.hip takes a product, by what the host knows of
+// it: sizes, strides and alignment.  Apart from the kernels, so that it can be looked at without a GPU.
+#pragma once
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "tsenor_ops_internal.h"
+
+namespace tsenor {
+
+enum Kind { kProduct, kGradient };
+
+// kFew64, kFew32, kFew16: 16 rows and that many columns a workgroup; kFew32x32: 32 of both; kStaged256x128:
+// rows that are not 16-byte aligned, through registers; kAny: any alignment and size; the others: tiles fed
+// by direct loads (columns x rows).
+enum Form { kFew64, kFew32, kFew16, kFew32x32, kAny, kStaged256x128, k256x256, k256x128, k128x128, k64x64 };
+
+constexpr int64_t kCus = 256;
+constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside a tile fit 32 bits
+
+// Direct loads take 16 bytes of an aligned row at a time.
+inline bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0;
+}
+
+// Tiles of a launch, as far as the host can know: a little more than half a tile counted for each expert.
+template <Kind K>
+int64_t tiles_of(const GroupedJob& job, int64_t m, int64_t n) {
+    const int64_t across = (job.inner + m - 1) / m;
+    return across * (K == kGradient ? (job.outer + n - 1) / n * job.experts
+                                    : (job.rows + n - 1) / n + (job.ends != nullptr ? job.experts * 9 / 16 : 0));
+}
+
+// The tile whose rounds of workgroups take the least time.  Measured, hundredths of a microsecond for a step
+// (64 bytes of the reduction) of one round: 256 x 256: 60; 256 x 128: 43; 128 x 128: 31; 64 x 64: 19 with one
+// workgroup on a CU, 28 with two (weight gradients: 27 and, with four, 50).  Examples (us), in that order: 1542 rows
+// 2048 x 5952 102 / 77 / 55 / 94; 600 rows 8192 x 4096 76 / 56 / 70 / 84; 600 rows of 16 experts 2048 x 4096
+// 95 / 89 / 67 / 77; 2048 rows of them 111 / 94 / 102 / 130; 4096 rows 116 / 153 / 146 / 203; data gradients, 200 rows of
+// 8 experts 2048 x 4096 62 / 55 / 40 / 27; 16384 rows of 8 experts 11008 x 4096 1252 / 1645 / 2047 / 3972.
+// A weight gradient's reduction is short, so that beginning and ending a tile counts too: 7, 6 and 4 us a round, and
+// 4 and 2.5 us once with a ring of more than 64 KB; where each workgroup has one tile, the largest expert's
+// rows count (taken as 1.6 times the mean), else a third of what they exceed it by.  Examples, 256 x 256 / 128 x
+// 128 / 64 x 64: 8192 rows 2048 x 2048 164 / 86 / 127; experts 1024 x 1024, 1024 rows of 4: 18 / 12 / 10, 4096 rows of
+// 8: 29 / 24 / 21, 8000 rows: 46 / 37 / 37, 8192 rows of 16: 35 / 45 / 44; 2048 rows of 16 experts 2048 x 2048 46 / 96 / 85.
+template <Kind K>
+Form pick_tile(const GroupedJob& job) {
+    const auto rounds = [&](int64_t m, int64_t n, int64_t at_once) {
+        return (tiles_of<K>(job, m, n) + at_once - 1) / at_once;
+    };
+    const double steps = K == kGradient ? job.rows / (32. * job.experts) : 1.;
+    const auto cost = [&](int64_t count, double step, double begin, double once) {
+        if (K == kProduct) return count * step;
+        return count * (step * steps * (job.experts == 1 ? 1. : count == 1 ? 1.6 : 1.2) + begin) + once;
+    };
+    Form best = k256x256;
+    double least = cost(rounds(256, 256, kCus), 60, 700, 400);
+    const auto take = [&](Form tile, double cost) {
+        if (cost < least) {
+            best = tile;
+            least = cost;
+        }
+    };
+    if (K == kProduct) take(k256x128, cost(rounds(256, 128, kCus), 43, 0, 0));
+    take(k128x128, cost(rounds(128, 128, kCus), 31, 600, 250));
+    const int64_t small = tiles_of<K>(job, 64, 64);
+    if (K == kProduct) take(k64x64, small <= kCus ? 19. : std::max(28., 28. * small / (2 * kCus)));  // not in rounds
+    else if (small <= kCus) take(k64x64, 27 * steps + 400);
+    else take(k64x64, rounds(64, 64, 4 * kCus) * (50 * steps + 400));  // a CU's four have different experts' rows
+    return best;
+}
+
+template <Kind K, bool AT, bool BT>
+Form pick_form(const GroupedJob& job, int size) {  // size: bytes of an operand's entry
+    if (K == kProduct && !AT) {
+        // Few rows: on average up to eight an expert, or up to 64 where tiles would leave CUs without work.
+        // Measured (us), 16 columns a wave / 64 x 64 tiles: 6 rows of 64 experts 1408 x 2048: 11 / 28; 64 rows:
+        // 47 / 47; 64 rows of 16 experts 2048 x 4096: 49 / 56; 16 rows 11008 x 4096: 21 / 24; 64 rows 4096 x
+        // 4096 18 / 25, 11008 x 4096 46 / 25.  As many columns as leave 160 workgroups: one row 4096 x 4096 in
+        // 11 / 13 / 19 for 16 / 32 / 64; 16 rows 11008 x 4096 in 26 / 28 / 21.
+        const int64_t parts = job.ends != nullptr ? std::min<int64_t>(job.rows, job.experts) : 1;
+        if (job.rows <= 16 || job.rows <= 8 * (int64_t)job.experts) {
+            if ((job.inner + 63) / 64 * parts >= 160) return kFew64;
+            if ((job.inner + 31) / 32 * parts >= 160) return kFew32;
+            return kFew16;
+        }
+        if (job.rows <= 64 && tiles_of<K>(job, 64, 64) < 128) return kFew32x32;
+    }
+    if (size == 2) {  // 8-bit integers are aligned, and their rows short
+        // tiles count rows, columns and the bytes between rows in 32 bits
+        if (job.inner > (K == kGradient ? 1 << 26 : 0x7FFFFF00) || job.outer > 0x7FFFFF00 || job.lda >= kMaxRow ||
+            job.ldb >= kMaxRow)
+            return kAny;
+        const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
+        if (!direct(job.a, job.lda, as, AT ? job.inner * size : job.kbytes) ||
+            !direct(job.b, job.ldb, 0, BT ? job.outer * size : job.kbytes)) {
+            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5850 / 3200; 1003 rows of 16
+            // experts 2047 x 4095: 132 / 157; column-contiguous operands, 8192 rows of 16 experts 4095 x 2047: 764 / 829,
+            // weight gradients 739 / 800.
+            return !AT && !BT && tiles_of<K>(job, 256, 128) >= 160 ? kStaged256x128 : kAny;
+        }
+    }
+    return pick_tile<K>(job);
+}
+
+}  // namespace tsenor
