@@ -870,7 +870,8 @@ int tile(const GroupedJob& job, void* stream) {
     const int64_t down = K == kGradient ? (job.outer + TN - 1) / TN * job.experts
                                         : most_row_tiles(job.rows, job.experts, TN, job.ends != nullptr);
     if (across > (int64_t)0xFFFFFFFF / (64 * WM * WN) / down) return kGridTooLarge;
-    const int64_t most = kCus * (sizeof(u32x4) * 4 * (TM + TN) * R > 72 * 1024 ? 1 : 2);  // by LDS
+    static_assert(sizeof(RowTable) == kRowTableBytes && sizeof(ExpertRows) == kExpertRowsBytes, "LDS");
+    const int64_t most = kCus * at_once(K, TM, TN, R);
     const int64_t groups = LONG && across * down > most ? most : across * down;
     hipLaunchKernelGGL((product_tile_kernel<T, AT, BT, K, TM, TN, WM, WN, R, LONG, DIRECT, TO>), dim3((unsigned)groups),
                        dim3(64 * WM * WN), 0, (hipStream_t)stream, job);

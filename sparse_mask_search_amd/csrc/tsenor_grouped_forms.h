@@ -19,6 +19,21 @@ enum Form { kFew64, kFew32, kFew16, kFew32x32, kAny, kStaged256x128, k256x256, k
 constexpr int64_t kCus = 256;
 constexpr int64_t kMaxRow = int64_t(1) << 23;  // bytes of a row: offsets inside a tile fit 32 bits
 
+// LDS of a tile's kernel whose workgroups walk over tiles: the ring (64 bytes of each row and column), the
+// experts' rows, and for a weight gradient two sets of its tile's mask words.
+constexpr int64_t kLdsOfCu = 160 * 1024;
+constexpr int64_t kMostExperts = 1024, kRowTableBytes = 3 * (kMostExperts + 1) * 4, kExpertRowsBytes = (kMostExperts + 64) * 4;
+constexpr int64_t tile_lds(Kind kind, int columns, int rows, int ring) {
+    return 64 * (int64_t)(columns + rows) * ring +
+           (kind == kProduct ? kRowTableBytes : kExpertRowsBytes + 2 * rows * (columns / 32) * 4);
+}
+// Workgroups of a CU at one time: 2 of 64 x 64, 1 of the others.  (Two of the staged 256 x 128 tile, whose ring
+// alone would let them in, run one after the other, each with half of the tiles: 16384 rows of 8 experts 11009 x
+// 4095 3210 us, one 2960; 8192 rows of 16 4095 x 2047 398, 385; 2000 rows 11009 x 4095 340, 345.)
+constexpr int64_t at_once(Kind kind, int columns, int rows, int ring) {
+    return kLdsOfCu / tile_lds(kind, columns, rows, ring);
+}
+
 // Direct loads take 16 bytes of an aligned row at a time.
 inline bool direct(const void* p, int64_t ld, int64_t stride, int64_t width) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0 && width % 16 == 0;
@@ -94,7 +109,7 @@ Form pick_form(const GroupedJob& job, int size) {  // size: bytes of an operand'
         const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
         if (!direct(job.a, job.lda, as, AT ? job.inner * size : job.kbytes) ||
             !direct(job.b, job.ldb, 0, BT ? job.outer * size : job.kbytes)) {
-            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5850 / 3200; 1003 rows of 16
+            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5850 / 2960; 1003 rows of 16
             // experts 2047 x 4095: 132 / 157; column-contiguous operands, 8192 rows of 16 experts 4095 x 2047: 764 / 829,
             // weight gradients 739 / 800.
             return !AT && !BT && tiles_of<K>(job, 256, 128) >= 160 ? kStaged256x128 : kAny;

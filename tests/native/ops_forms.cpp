@@ -32,3 +32,9 @@ int hip_error(int, const char*) { return TSENOR_ERR_HIP; }
 }  // namespace tsenor
 
 extern "C" const char* last_form() { return form; }
+extern "C" int64_t lds_of_tile(int gradient, int columns, int rows, int ring) {
+    return tsenor::tile_lds(gradient ? tsenor::kGradient : tsenor::kProduct, columns, rows, ring);
+}
+extern "C" int64_t workgroups_of_cu(int gradient, int columns, int rows, int ring) {
+    return tsenor::at_once(gradient ? tsenor::kGradient : tsenor::kProduct, columns, rows, ring);
+}

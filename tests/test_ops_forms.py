@@ -3,12 +3,15 @@ entry points (tests/native/ops_forms.cpp), held to the sizes of tests/ops_sizes.
 sizes whose results tests/test_gpu_ops_forms.py compares."""
 import ctypes
 import os
+import re
 import shutil
+import struct
 import subprocess
 
 import pytest
 
 import ops_sizes as sizes
+import sparse_mask_search_amd as sms
 from sparse_mask_search_amd import build
 
 pytestmark = pytest.mark.skipif(shutil.which(build.hipcc()) is None and not os.path.exists(build.hipcc()),
@@ -27,6 +30,7 @@ def rule(tmp_path_factory):
         os.path.join(build.CSRC, "tsenor_ops_abi.cpp")], stderr=subprocess.DEVNULL)
     l = ctypes.CDLL(so)
     l.last_form.restype = ctypes.c_char_p
+    l.lds_of_tile.restype = l.workgroups_of_cu.restype = Q
     l.tsenor_grouped_mm.argtypes = [P, Q, Q, P, I, Q, Q, Q, Q, Q, P, P, I, Q, P]
     l.tsenor_grouped_wgrad.argtypes = [P, Q, P, Q, Q, Q, Q, Q, P, P, P, I, Q, Q, P]
     l.tsenor_gemm_int8.argtypes = [P, I, P, Q, Q, P, P, Q, Q, Q, P, P, I, Q, P]
@@ -103,3 +107,44 @@ def test_half_tiles_in_both_places(op):
             halves = sum(0 < n % tall <= tall // 2 for n in counts)
             last[across * (c[1] // tall) < 4 * groups] += halves if tall > 64 else 0
     assert last[True] > 0 and last[False] > 0, last
+
+
+def kernels_of_the_library(tmp_path):
+    """(name, LDS bytes, vector registers, threads) of every kernel in the library as it was built."""
+    readelf = os.path.join(os.path.dirname(os.path.dirname(build.hipcc())), "llvm", "bin", "llvm-readelf")
+    if not os.path.exists(readelf):
+        pytest.skip("llvm-readelf is not installed")
+    data, magic, at, found = open(sms.library_path(), "rb").read(), b"__CLANG_OFFLOAD_BUNDLE__", 0, []
+    while (at := data.find(magic, at)) >= 0:
+        (entries,), entry = struct.unpack_from("<Q", data, at + 24), at + 32
+        for _ in range(entries):
+            first, size, length = struct.unpack_from("<QQQ", data, entry)
+            if b"gfx950" in data[entry + 24:entry + 24 + length] and size:
+                obj = tmp_path / "object"
+                obj.write_bytes(data[at + first:at + first + size])
+                notes = subprocess.check_output([readelf, "--notes", str(obj)], text=True)
+                for part in notes.split("  - .agpr_count")[1:]:
+                    field = lambda key: re.search(rf"\.{key}:\s+(\S+)", part).group(1)
+                    found.append((field("name"), int(field("group_segment_fixed_size")), int(field("vgpr_count")),
+                                  int(field("max_flat_workgroup_size"))))
+            entry += 24 + length
+        at += len(magic)
+    return found
+
+
+def test_workgroups_at_once_fit_a_cu(rule, tmp_path):
+    """As many workgroups walk over tiles as a CU holds at one time, by its 160 KB of LDS and its registers (512 a
+    lane of each of four SIMDs): more would begin when the first ones have ended."""
+    pattern = re.compile(r"product_tile_kernelI.*?KindE(\d)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELb(\d)E")
+    seen = set()
+    for name, lds, registers, threads in kernels_of_the_library(tmp_path):
+        if (m := pattern.search(name)) is None or m.group(7) == "0":
+            continue
+        gradient, columns, rows, _, _, ring = map(int, m.groups()[:6])
+        seen.add((gradient, columns, rows, ring))
+        assert lds <= rule.lds_of_tile(gradient, columns, rows, ring) + 64 and lds > 64 * (columns + rows) * ring, name
+        count = rule.workgroups_of_cu(gradient, columns, rows, ring)
+        waves = 4 * (512 // (-(-registers // 8) * 8))
+        assert count == min(160 * 1024 // lds, waves // (threads // 64)), (name, lds, registers, count)
+    assert seen == {(0, 256, 256, 4), (0, 256, 128, 6), (0, 128, 128, 8), (0, 64, 64, 8), (0, 256, 128, 3),
+                    (1, 256, 256, 4), (1, 128, 128, 8)}
