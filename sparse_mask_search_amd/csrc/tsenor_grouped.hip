@@ -23,18 +23,17 @@ typedef __attribute__((address_space(1))) const uint8_t global_byte;
 __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
     return *(__attribute__((address_space(1))) const any16*)(global_byte*)p;
 }
-// The same of which `valid` are there; zeros behind them.
-template <class T>
+// The same of bf16 entries of which `valid` bytes are there; zeros behind them.  (Rows of 8-bit integers are whole
+// units.)
 __device__ __forceinline__ u32x4 load16(const uint8_t* p, int64_t valid) {
     if (valid >= 16) return load16(p);
     u32x4 v = {0u, 0u, 0u, 0u};
     if (valid > 0) {
 #pragma unroll
-        for (int i = 0; i < 16 / T::kSize; ++i)
-            if (i * T::kSize < valid) {
-                const uint32_t x = T::kSize == 2 ? ((__attribute__((address_space(1))) const uint16_t*)(global_byte*)p)[i]
-                                                 : ((global_byte*)p)[i];
-                v[i * T::kSize / 4] |= x << (8 * (i * T::kSize % 4));
+        for (int i = 0; i < 8; ++i)
+            if (2 * i < valid) {
+                const uint32_t x = ((__attribute__((address_space(1))) const uint16_t*)(global_byte*)p)[i];
+                v[i / 2] |= x << (16 * (i % 2));
             }
     }
     return v;
@@ -70,6 +69,7 @@ __device__ __forceinline__ void finish(const GroupedJob& job, int expert, int64_
 // by the tiles below, 161).
 template <class T, bool AT, bool BT, Kind K, class TO>
 __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) {
+    static_assert(T::kSize == 2, "rows of 8-bit integers are aligned");
     __shared__ u32x4 ta[2][256], tb[2][256];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -115,10 +115,10 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
         if (!turned) {
             const int r = tid >> 2;
             const int64_t c = 64 * (int64_t)s + 16 * (tid & 3);
-            return load16<T>(base + min((int64_t)r, have - 1) * ld + c, reduce - c);
+            return load16(base + min((int64_t)r, have - 1) * ld + c, reduce - c);
         }
         const int r = 32 * s + (tid >> 3), c = 8 * (tid & 7);
-        return load16<T>(base + r * ld + c * T::kSize, r * T::kSize < reduce ? (have - c) * T::kSize : 0);
+        return load16(base + r * ld + c * T::kSize, r * T::kSize < reduce ? (have - c) * T::kSize : 0);
     };
     const int slot_row = row_slot(tid >> 2, tid & 3), slot_turned = turned_slot<64>(tid >> 3, tid & 7);
     typename T::Sum acc[2][2];
@@ -172,6 +172,7 @@ constexpr int kFewEntries = kMaxTokenEntries;  // of tokens in LDS, padded rows
 
 template <class T, bool QX, int NT, int MT, class TO>
 __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const GroupedJob job) {
+    constexpr bool kWhole = T::kSize == 1;  // units only
     constexpr int kAhead = NT * MT >= 4 ? 1 : NT * MT >= 2 ? 2 : 4;  // more registers would leave a CU one workgroup
     typedef typename T::Sum Sum4;
     __shared__ Sum4 sums[kFewWaves][MT * NT][64];
@@ -219,8 +220,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
                 const uint8_t* p = arow[m] + 128 * (int64_t)v;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (v < whole) av[i][m][c] = load16(p + 16 * c);
-                    else av[i][m][c] = load16<T>(p + 16 * c, job.kbytes - 128 * (int64_t)v - 32 * q - 16 * c);
+                    if (kWhole || v < whole) av[i][m][c] = load16(p + 16 * c);
+                    else av[i][m][c] = load16(p + 16 * c, job.kbytes - 128 * (int64_t)v - 32 * q - 16 * c);
                 }
             }
         }
@@ -275,8 +276,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
                         bv[i][n][c] = token[min(16 * n + l16, rows - 1) * pitch + 8 * v + 2 * q + c];
                     } else {
                         const uint8_t* p = brow[n] + 128 * (int64_t)v + 16 * c;
-                        if (v < whole) bv[i][n][c] = load16(p);
-                        else bv[i][n][c] = load16<T>(p, job.kbytes - 128 * (int64_t)v - 32 * q - 16 * c);
+                        if (kWhole || v < whole) bv[i][n][c] = load16(p);
+                        else bv[i][n][c] = load16(p, job.kbytes - 128 * (int64_t)v - 32 * q - 16 * c);
                     }
                 }
         }
@@ -392,7 +393,7 @@ struct Loads {
         const uint8_t* p = of.base + s * of.step + of.offset[j];
         if (inside) return load16(p);
         const int slot = 64 * (wave * kCount + j) + lane, r = slot / 4;
-        return load16<T>(p, reduce - 64 * s - 16 * (row_slot(r, slot % 4) - 4 * r));
+        return load16(p, reduce - 64 * s - 16 * (row_slot(r, slot % 4) - 4 * r));
     }
     __device__ static __forceinline__ void store(u32x4* tile, int j, u32x4 v, int wave, int lane) {
         tile[64 * (wave * kCount + j) + lane] = v;
@@ -539,7 +540,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
     typedef Loads<T, BT, TN, W> LoadsB;
     constexpr bool kMasked = K == kGradient && LONG;
     constexpr int kHalf = TB > 1 ? TN / 2 : 0;  // an expert's last rows, if they are no more, take half a tile's products
-    static_assert(DIRECT ? R >= 4 : R == 3 && !AT && !BT, "ring");
+    static_assert(DIRECT ? R >= 4 : R == 3 && !AT && !BT && T::kSize == 2, "ring");
     struct Buffer {
         u32x4 a[TM * 4];
         u32x4 b[TN * 4];
