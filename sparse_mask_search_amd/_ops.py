@@ -104,6 +104,8 @@ def grouped_mm(torch, X, W, ends, transpose: bool = False, out=None, dtype=None)
     yt = _float_type(torch, out, "out")
     if rows == 0 or m == 0:
         return out
+    if k == 0 or experts == 0:
+        raise ValueError("X has no columns" if k == 0 else "W holds no expert")
     stride, ldw = _stack_strides(W)
     _run(torch, "tsenor_grouped_mm", device, lib().tsenor_grouped_mm, X.data_ptr(), rows, _ld(X), W.data_ptr(),
          1 if transpose else 0, experts, stride, ldw, m, k, ends.data_ptr(), out.data_ptr(), yt, _ld(out))
@@ -199,6 +201,8 @@ def gemm_int8(torch, X, A, ends=None, out=None, dtype=None):
     yt = _float_type(torch, out, "out")
     if rows == 0 or m == 0:
         return out
+    if k == 0 or experts == 0:
+        raise ValueError("X has no columns" if k == 0 else "A holds no expert")
     if ready:
         x, xtype, xs, ldx = X.values.data_ptr(), INT8, X.scales.data_ptr(), X.values.shape[1]
     elif xt == BF16 and ends is None and rows <= 16 and rows * _pad(k) <= 32768:

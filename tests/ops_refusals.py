@@ -46,6 +46,9 @@ def calls(device, sms):
         ("out over X", "grouped_mm", (wide[:, :32], w, ends), dict(out=wide[:, 31:95]), V, "out overlaps an input"),
         ("out over W", "grouped_mm", (x, w, ends), dict(out=w.view(-1)[:2560].view(40, 64)), V, "out overlaps an input"),
         ("out over ends", "grouped_mm", (x, w, y.view(-1).view(i32)[8:12]), dict(out=y), V, "out overlaps an input"),
+        ("X without columns", "grouped_mm", (x[:, :0], w[:, :, :0], ends), {}, V, "X has no columns"),
+        ("transposed, X without columns", "grouped_mm", (x[:, :0], w[:, :0], ends), dict(transpose=True), V, "X has no columns"),
+        ("no expert", "grouped_mm", (x, w[:0], ends[:0]), {}, V, "W holds no expert"),
         # weight gradients
         ("dY not bf16", "grouped_wgrad", (dy.float(), x, ends), {}, T, "dY must be bfloat16"),
         ("dY of fewer rows", "grouped_wgrad", (dy[:-1], x, ends), {}, V, "dY has 39 rows, X has 40"),
@@ -82,6 +85,9 @@ def calls(device, sms):
         ("out over A's scales", "gemm_int8", (x, a._replace(scales=y.view(-1).view(f32)[4:68])), dict(out=y), V, "out overlaps an input"),
         ("out over X's scales", "gemm_int8", (q._replace(scales=y.view(-1).view(f32)[4:44]), a), dict(out=y), V, "out overlaps an input"),
         ("out of fewer columns", "gemm_int8", (x, a), dict(out=y[:, 1:]), V, r"out must be a tensor of shape \(40, 64\)"),
+        ("X without columns", "gemm_int8", (x[:, :0], sms.DenseInt8(a.values[:, :0], a.scales, 0)), {}, V, "X has no columns"),
+        ("integers without columns", "gemm_int8", (sms.DenseInt8(q.values[:, :0], q.scales, 0), sms.DenseInt8(a.values[:, :0], a.scales, 0)), {}, V, "X has no columns"),
+        ("no expert", "gemm_int8", (x, sms.DenseInt8(ae.values[:0], ae.scales[:0], 32)), dict(ends=ends[:0]), V, "A holds no expert"),
         # gradients
         ("a gradient twice", "clip_grads", ([x, x], 1.0), {}, V, "a gradient that is written overlaps"),
         ("a gradient and rows of it", "clip_grads", ([x, x[3:5]], 1.0), {}, V, "a gradient that is written overlaps"),
