@@ -18,6 +18,16 @@ from ._lib import BF16, F32, lib
 INT8 = 3
 
 
+def _in_one_launch(rows, k, m):
+    """Whether bf16 tokens become integers inside the product: every workgroup of 16 columns does it for itself, which
+    costs 0.8 us a further token up to 4096 columns (a workgroup for each CU), 1.9 at 11008 and 4.2 at 32000;
+    a launch of its own costs 3 us, and 5 of the host's.  Measured (us), inside / before: called one by one 1 token
+    4096 x 4096 9.5 / 14.3, 4 tokens 10.2 / 14.0, 8 tokens 14.4 / 14.0, 16 tokens 4096 x 2048 18.7 / 14.0, 3 tokens 11008 x
+    4096 16.1 / 16.0, 1 token 32000 x 4096 27.7 / 30.4, 2 tokens 32.7 / 30.5; in a graph, the same, 7.7 / 10.3,
+    10.3 / 10.9, 14.6 / 11.1, 18.8 / 9.9, 16.6 / 16.8, 29.0 / 31.2, 33.3 / 31.4.  Calls one by one set the bound."""
+    return (rows == 1 or rows <= 8 and rows * m <= 32768) and rows * _pad(k) <= 32768
+
+
 class DenseInt8(NamedTuple):
     """8-bit integer operand [rows, k] (or a stack [experts, rows, k]): values int8
     [.., rows, kpad], scales fp32 [.., rows]; a row stands for values * scale."""
@@ -205,7 +215,7 @@ def gemm_int8(torch, X, A, ends=None, out=None, dtype=None):
         raise ValueError("X has no columns" if k == 0 else "A holds no expert")
     if ready:
         x, xtype, xs, ldx = X.values.data_ptr(), INT8, X.scales.data_ptr(), X.values.shape[1]
-    elif xt == BF16 and ends is None and rows <= 16 and rows * _pad(k) <= 32768:
+    elif xt == BF16 and ends is None and _in_one_launch(rows, k, m):
         x, xtype, xs, ldx = X.data_ptr(), BF16, None, _ld(X)
     else:  # quantised into one buffer, scales behind the values
         ldx = _pad(k)
