@@ -22,9 +22,10 @@ def _in_one_launch(rows, k, m):
     """Whether bf16 tokens become integers inside the product: every workgroup of 16 columns does it for itself, which
     costs 0.8 us a further token up to 4096 columns (a workgroup for each CU), 1.9 at 11008 and 4.2 at 32000;
     a launch of its own costs 3 us, and 5 of the host's.  Measured (us), inside / before: called one by one 1 token
-    4096 x 4096 9.5 / 14.3, 4 tokens 10.2 / 14.0, 8 tokens 14.4 / 14.0, 16 tokens 4096 x 2048 18.7 / 14.0, 3 tokens 11008 x
-    4096 16.1 / 16.0, 1 token 32000 x 4096 27.7 / 30.4, 2 tokens 32.7 / 30.5; in a graph, the same, 7.7 / 10.3,
-    10.3 / 10.9, 14.6 / 11.1, 18.8 / 9.9, 16.6 / 16.8, 29.0 / 31.2, 33.3 / 31.4.  Calls one by one set the bound."""
+    4096 x 4096 9.5 / 14.3, 4 tokens 10.2 / 14.0, 8 tokens 14.4 / 14.0, 12 tokens 512 x 512 12.7 / 14.1, 16 tokens 4096 x 2048
+    18.7 / 14.0, 3 tokens 11008 x 4096 16.1 / 16.0, 1 token 32000 x 4096 27.7 / 30.4, 2 tokens 32.7 / 30.5; in a graph, the
+    same, 7.7 / 10.3, 10.3 / 10.9, 14.6 / 11.1, 12.2 / 6.2, 18.8 / 9.9, 16.6 / 16.8, 29.0 / 31.2, 33.3 / 31.4.  Past four
+    tokens a graph wants the launch and calls one by one do not: eight lie between."""
     return (rows == 1 or rows <= 8 and rows * m <= 32768) and rows * _pad(k) <= 32768
 
 

@@ -9,6 +9,9 @@
 // Memory bounds both: four layers of a model of width 4096 (810M bf16 entries under masks) 331 us for the sums
 // (5.2 TB/s) and 731 for the scaling (4.6 TB/s, reading and writing).  One layer of width 64 takes 6.5 us each,
 // which is latency: arguments, entries, the workgroup's sum.
+// Adding all partial sums in every workgroup of every scaling launch is quadratic in the list.  It shows where thousands
+// of tensors have many chunks each: scaling tensors of 1408 x 2048 in bf16 to others runs at 5.4 TB/s for 480 of them, 5.1 for
+// 1920, 4.6 for 4800 and 3.8 for 9600 (the sums at 5.0 to 5.1); a stack of them is one tensor.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -78,8 +81,9 @@ __device__ __forceinline__ T scaled_one(const T* p, bool keep, float f) {
     else return keep ? *p * f : 0.f;
 }
 
-// Results leave past the caches, which keep gradients for the scaling instead: 810M bf16 entries 880 ->
-// 838 us, under masks 1091 -> 1059.  fp32 results do not (405M entries under masks 940 -> 955).
+// Results leave past the caches, which keep gradients for the scaling instead: 810M bf16 entries to other
+// tensors 881 -> 839 us, under masks 1095 -> 1060; in place 908 and 1109 either way.  fp32 results do not (405M entries under
+// masks 944 -> 957, without 919 -> 966).
 template <class T>
 __device__ __forceinline__ void store_last(const Eight<T>& v, T* to) {
     if constexpr (sizeof(T) == 2)

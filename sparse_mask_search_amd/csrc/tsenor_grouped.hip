@@ -65,8 +65,8 @@ __device__ __forceinline__ void finish(const GroupedJob& job, int expert, int64_
 
 // Any alignment and any size: tiles of 64 x 64, four waves of 32 x 32, operands through
 // registers into two LDS buffers.  AT, BT: the operand is contiguous along its columns.  Loads that straddle
-// lines bound it: 8192 rows of 16 experts 4095 x 2047, data gradients 764 us (180 TFLOP/s; 16-byte aligned rows,
-// by the tiles below, 161).
+// lines bound it: 8192 rows of 16 experts 4095 x 2047, data gradients 806 us (170 TFLOP/s; 16-byte aligned rows,
+// by the tiles below, 164).
 template <class T, bool AT, bool BT, Kind K, class TO>
 __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) {
     static_assert(T::kSize == 2, "rows of 8-bit integers are aligned");
@@ -158,15 +158,15 @@ __global__ __launch_bounds__(256) void product_any_kernel(const GroupedJob job) 
     }
 }
 
-// Few rows (16 NT of one expert to a workgroup): reading the weights bounds the product (6 rows of 64 experts
-// 1408 x 2048 11 us, 3.1 TB/s of them; 16 rows 11008 x 4096 21 us, 4.3 TB/s), so a
+// Few rows (16 NT of one expert to a workgroup): reading the weights bounds the product (16 rows 11008 x 4096 25 us,
+// 3.6 TB/s of them; 6 rows of 64 experts 1408 x 2048 12 us, of which 4 are the launch and `ends`: k = 128), so a
 // workgroup owns 16 MT columns of the output (rows of the weights) and each of its eight waves
 // a stretch of the reduction, with the loads of kAhead units of 128 bytes in flight; the waves'
 // sums meet in LDS, in wave order.  A lane q = lane / 16 takes bytes 32 q .. 32 q + 31 of a unit of
 // both operands: the two instructions may take the reduction in any order that is the same for both.
 // QX: bf16 tokens become 8-bit integers in LDS first, in each workgroup, while its first weights are
 // loaded (as fragments, each lane for itself, 16 lanes would do the same work: 12 us for one token
-// 4096 x 4096, against 7).
+// 4096 x 4096, against 7.7; 7.5 from ready integers).
 constexpr int kFewWaves = 8;
 constexpr int kFewEntries = kMaxTokenEntries;  // of tokens in LDS, padded rows
 
@@ -327,11 +327,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(const Group
 // would stall every wave on the address unit.  Rows and columns behind an operand's end
 // repeat its last one (nothing of them is stored); behind the reduction's end zeros are loaded.
 // As many workgroups as the LDS holds walk over the tiles, so that the ring never runs empty between two.
-// Measured: 8192 x 8192 x 8192 807 us, 1.36 PFLOP/s, the matrix cores 74% busy at 1.50 GHz: the card's power bounds it
-// (the plain library product 758 us).  16384 rows of 8 experts 11008 x 4096 1.26 ms (1.17 PFLOP/s), 8192 of 8-bit
-// integers 358 us (2.06 POP/s): the last round of tiles too.  8192 rows of 16 experts 2048 x 4096: data gradients
-// 161 us (44% busy at 2.1 GHz; 127 with as many rows for each), weight gradients under masks 161 us, of which 42 us are
-// the results' way out: a step's wait is for the stores before it too.
+// Measured: 8192 x 8192 x 8192 806 us, 1.36 PFLOP/s, the matrix cores 74% busy at 1.50 GHz, which the card's power
+// sets (the plain library product 689 us on the same inputs).  16384 rows of 8 experts 11008 x 4096 1.27 ms (1.16 PFLOP/s),
+// 8192 of 8-bit integers 360 us (2.05 POP/s): the last round of tiles too.  8192 rows of 16 experts 2048 x 4096: data
+// gradients 164 us (44% busy at 2.1 GHz; 127 with as many rows for each), weight gradients under masks 178 us, of which 47
+// are the results' way out: a step's wait is for the stores before it too.  (The last from seven inputs in turn, 700 MB;
+// 162 from one, which the last-level cache holds.  The cut of the rows counts for less: 175 to 184 over four.)
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
@@ -405,7 +406,8 @@ struct Loads {
 };
 
 // Weight gradients, the largest part of what such a call moves, leave past the caches: 8192 rows of 16
-// experts 2048 x 4096 168 -> 161 us.  A product's results do not (8192 x 4096 over 1024: 60 -> 64 us).
+// experts 2048 x 4096 under masks 183 -> 178 us, 1022 rows of 16 1792 x 7680 in fp32 192 -> 180 (under masks 239 -> 244).
+// A product's results do not (8192 x 4096 over 1024: 69 -> 72 us).
 template <Kind K, class V>
 __device__ __forceinline__ void put_last(V* to, V v) {
     if constexpr (K == kGradient) __builtin_nontemporal_store(v, to);
@@ -473,8 +475,8 @@ __device__ __forceinline__ void store_tile(const GroupedJob& job, int expert, in
     };
     constexpr int kPiece = kHalf ? 2 : 1;         // tiles of one
     // Two pieces to each store, whole lines of 8 rows, for weight gradients: 1022 rows of 16 experts 1792 x
-    // 7680 in fp32 298 -> 178 us (5.1 TB/s), 8192 rows of 16 2048 x 4096 216 -> 193, in bf16 164 -> 161.  Products, whose
-    // results are a smaller part, gain nothing.
+    // 7680 in fp32 297 -> 180 us (5.1 TB/s), 8192 rows of 16 2048 x 4096 under masks 272 -> 230, in bf16 192 -> 178.
+    // Products, whose results are a smaller part, gain nothing.
     constexpr bool kLines = K == kGradient && FA % (2 * kPiece) == 0;
     const int l16 = threadIdx.x & 15, col = kHalf ? 16 * (q & 1) + 8 * (q >> 1) : 4 * q;
     TO* y = out + (kLines ? row0 - (l16 & 8) : row0) * job.ldo + c0 + col + (kLines ? (l16 >> 3) * 16 * kPiece : 0);
@@ -571,9 +573,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_tile_kernel(const Groupe
         static_assert(LONG, "products");
         const RowTable& table = lds<RowTable>();
         // Half tiles go behind all others where workgroups have few tiles, so that none begins a whole one last: 8192
-        // rows of 16 experts 2048 x 4096 204 -> 189 us, 4096 x 2048 transposed 166 -> 161, 4096 rows of 8 11008 x 4096 416 ->
-        // 426.  With more they are farther from those that read the same weights, for nothing: 16384 rows of 8
-        // experts 11008 x 4096 1253 -> 1266 us.
+        // rows of 16 experts 2048 x 4096 210 -> 197 us, 4096 x 2048 transposed 169 -> 164, but 4096 rows of 8 11008 x 4096
+        // 412 -> 432.  With more they are farther from those that read the same weights, for nothing: 16384 rows of 8
+        // experts 11008 x 4096 1269 -> 1276 us.
         const bool last = across * (int64_t)(job.rows / TN) < 4 * (int64_t)gridDim.x;
         row_table(job.ends, job.experts, job.rows, TN, last ? kHalf : 0, lds<RowTable>());
         __syncthreads();

@@ -9,6 +9,8 @@
 
 namespace tsenor {
 
+// Times here are of graphs that take three to twelve inputs in turn, more than the last-level cache holds.
+
 enum Kind { kProduct, kGradient };
 
 // kFew64, kFew32, kFew16: 16 rows and that many columns a workgroup; kFew32x32: 32 of both; kStaged256x128:
@@ -49,15 +51,16 @@ int64_t tiles_of(const GroupedJob& job, int64_t m, int64_t n) {
 
 // The tile whose rounds of workgroups take the least time.  Measured, hundredths of a microsecond for a step
 // (64 bytes of the reduction) of one round: 256 x 256: 60; 256 x 128: 43; 128 x 128: 31; 64 x 64: 19 with one
-// workgroup on a CU, 28 with two (weight gradients: 27 and, with four, 50).  Examples (us), in that order: 1542 rows
-// 2048 x 5952 102 / 77 / 55 / 94; 600 rows 8192 x 4096 76 / 56 / 70 / 84; 600 rows of 16 experts 2048 x 4096
-// 95 / 89 / 67 / 77; 2048 rows of them 111 / 94 / 102 / 130; 4096 rows 116 / 153 / 146 / 203; data gradients, 200 rows of
-// 8 experts 2048 x 4096 62 / 55 / 40 / 27; 16384 rows of 8 experts 11008 x 4096 1252 / 1645 / 2047 / 3972.
+// workgroup on a CU, 28 with two (weight gradients: 27 and, with four, 50).  (One or two inputs in turn, which the
+// last-level cache holds: what a step costs.)  Examples (us), in that order: 1542 rows 2048 x 5952 122 / 100 / 69 / 111;
+// 600 rows 8192 x 4096 87 / 78 / 95 / 110; 600 rows of 16 experts 2048 x 4096 95 / 90 / 71 / 80; 1003 rows 103 / 92 / 92 / 85,
+// where the rule takes the second; 2048 rows 112 / 96 / 108 / 127; 4096 rows 115 / 155 / 147 / 210; data gradients, 200
+// rows of 8 experts 2048 x 4096 68 / 60 / 44 / 38; 16384 rows of 8 experts 11008 x 4096 1268 / 1681 / 2053 / 4168.
 // A weight gradient's reduction is short, so that beginning and ending a tile counts too: 7, 6 and 4 us a round, and
 // 4 and 2.5 us once with a ring of more than 64 KB; where each workgroup has one tile, the largest expert's
 // rows count (taken as 1.6 times the mean), else a third of what they exceed it by.  Examples, 256 x 256 / 128 x
-// 128 / 64 x 64: 8192 rows 2048 x 2048 164 / 86 / 127; experts 1024 x 1024, 1024 rows of 4: 18 / 12 / 10, 4096 rows of
-// 8: 29 / 24 / 21, 8000 rows: 46 / 37 / 37, 8192 rows of 16: 35 / 45 / 44; 2048 rows of 16 experts 2048 x 2048 46 / 96 / 85.
+// 128 / 64 x 64: 8192 rows 2048 x 2048 166 / 88 / 154; experts 1024 x 1024, 1024 rows of 4: 19 / 13 / 9, 4096 rows of
+// 8: 30 / 24 / 22, 8000 rows: 49 / 37 / 44, 8192 rows of 16: 42 / 44 / 50; 2048 rows of 16 experts 2048 x 2048 47 / 97 / 83.
 template <Kind K>
 Form pick_tile(const GroupedJob& job) {
     const auto rounds = [&](int64_t m, int64_t n, int64_t at_once) {
@@ -89,10 +92,12 @@ template <Kind K, bool AT, bool BT>
 Form pick_form(const GroupedJob& job, int size) {  // size: bytes of an operand's entry
     if (K == kProduct && !AT) {
         // Few rows: on average up to eight an expert, or up to 64 where tiles would leave CUs without work.
-        // Measured (us), 16 columns a wave / 64 x 64 tiles: 6 rows of 64 experts 1408 x 2048: 11 / 28; 64 rows:
-        // 47 / 47; 64 rows of 16 experts 2048 x 4096: 49 / 56; 16 rows 11008 x 4096: 21 / 24; 64 rows 4096 x
-        // 4096 18 / 25, 11008 x 4096 46 / 25.  As many columns as leave 160 workgroups: one row 4096 x 4096 in
-        // 11 / 13 / 19 for 16 / 32 / 64; 16 rows 11008 x 4096 in 26 / 28 / 21.
+        // Measured (us), 16 columns a wave / 64 x 64 tiles: 6 rows of 64 experts 1408 x 2048: 12 / 17; 64 rows:
+        // 49 / 52; 512 rows: 72 / 82; 64 rows of 16 experts 2048 x 4096: 52 / 58; 16 rows 11008 x 4096: 25 / 26; 64 rows
+        // 4096 x 4096 19 / 29, 11008 x 4096 50 / 32.  The host knows the average only: where all 512 rows are one of
+        // the 64 experts', its weights are read again for each 16 rows, and tiles would be faster: 31 / 17.  As many
+        // columns as leave 160 workgroups: one row 4096 x 4096 in 10 / 14 / 21 for 16 / 32 / 64; 16 rows 11008 x 4096 in
+        // 29 / 30 / 25.
         const int64_t parts = job.ends != nullptr ? std::min<int64_t>(job.rows, job.experts) : 1;
         if (job.rows <= 16 || job.rows <= 8 * (int64_t)job.experts) {
             if ((job.inner + 63) / 64 * parts >= 160) return kFew64;
@@ -109,9 +114,9 @@ Form pick_form(const GroupedJob& job, int size) {  // size: bytes of an operand'
         const int64_t as = (K == kGradient || job.experts == 1) ? 0 : job.astride;
         if (!direct(job.a, job.lda, as, AT ? job.inner * size : job.kbytes) ||
             !direct(job.b, job.ldb, 0, BT ? job.outer * size : job.kbytes)) {
-            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5850 / 2960; 1003 rows of 16
-            // experts 2047 x 4095: 132 / 157; column-contiguous operands, 8192 rows of 16 experts 4095 x 2047: 764 / 829,
-            // weight gradients 739 / 800.
+            // Tiles of 64 x 64 / 256 x 128 (us): 16384 rows of 8 experts 11009 x 4095: 5860 / 2990; 1003 rows of 16
+            // experts 2047 x 4095: 137 / 158; column-contiguous operands, 8192 rows of 16 experts 4095 x 2047, one input:
+            // 764 / 829, weight gradients 739 / 800 (with many inputs 806 and 696 by 64 x 64).
             return !AT && !BT && tiles_of<K>(job, 256, 128) >= 160 ? kStaged256x128 : kAny;
         }
     }
