@@ -3,30 +3,15 @@
 // here allocates or is kept between calls.
 #include <hip/hip_runtime.h>
 
+#include "tsenor_checks.h"
 #include "tsenor_fp8.h"
 #include "tsenor_internal.h"
 
 namespace {
 
-// Operands of at most this many entries keep every offset and every count of workgroups
-// inside int64; whether the workgroups fit one launch is for the launch functions (grid_fits).
-constexpr int64_t kMaxEntries = int64_t(1) << 40;
+using namespace tsenor;
 
-bool misaligned(const void* p, uintptr_t bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
-}
 int64_t blocks128(int64_t v) { return (v + 127) / 128; }
-// rows x cols entries, each padded by up to `pad`, without overflow
-bool too_big(int64_t rows, int64_t cols, int64_t pad = 0) {
-    return rows > kMaxEntries || cols > kMaxEntries || (cols > 0 && rows + pad > kMaxEntries / (cols + pad));
-}
-bool float_type(int t) { return t == TSENOR_F32 || t == TSENOR_BF16; }
-uintptr_t element_size(int t) { return t == TSENOR_F32 ? 4 : 2; }
-
-int status(int e, const char* where) {
-    if (e == tsenor::kGridTooLarge) return TSENOR_ERR_SHAPE;
-    return e == hipSuccess ? TSENOR_OK : tsenor::hip_error(e, where);
-}
 
 }  // namespace
 

@@ -3,6 +3,7 @@
 // here allocates or is kept between calls.
 #include <hip/hip_runtime.h>
 
+#include "tsenor_checks.h"
 #include "tsenor_internal.h"
 #include "tsenor_ops.h"
 #include "tsenor_ops_internal.h"
@@ -11,24 +12,13 @@ namespace {
 
 using namespace tsenor;
 
-constexpr int64_t kMaxEntries = int64_t(1) << 40, kMaxRows = int64_t(1) << 30, kMaxReduce = int64_t(1) << 17;
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxReduce = int64_t(1) << 17;
 constexpr int64_t kMaxExperts = 1024;
 
-bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
-bool too_big(int64_t rows, int64_t cols) {
-    return rows > kMaxEntries || cols > kMaxEntries || (cols > 0 && rows > kMaxEntries / cols);
-}
-bool float_type(int t) { return t == TSENOR_F32 || t == TSENOR_BF16; }
-int64_t element_size(int t) { return t == TSENOR_F32 ? 4 : 2; }
 // rows of four neighbouring entries may be written at once
 bool four(const void* p, int type, int64_t ld) { return !misaligned(p, 4 * element_size(type)) && ld % 4 == 0; }
 // rows of eight bf16 entries
 bool eight(const void* p, int64_t ld) { return !misaligned(p, 16) && ld % 8 == 0; }
-
-int status(int e, const char* where) {
-    if (e == kGridTooLarge) return TSENOR_ERR_SHAPE;
-    return e == hipSuccess ? TSENOR_OK : hip_error(e, where);
-}
 
 // Whether a gradient is one that the kernels can take.
 int grad_check(const tsenor_grad& g, bool write) {
